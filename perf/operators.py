@@ -249,7 +249,7 @@ def _prepare_attend(c, gen, rng):
     if own:
         from free_ffn_activation_b200 import decode
         s["cache"] = _own_cache(s)
-        s["ws"] = decode.attention_workspace(s["cache"], c["n"], s["max_q"], heads)
+        s["ws"] = decode.attention_workspace(s["cache"], s["max_q"], heads)
     return s
 
 
@@ -309,11 +309,7 @@ def _prepare_score(c, gen):
     logits.scatter_add_(1, at, torch.rand((c["rows"], 4), device="cuda", generator=gen) * 12)
     tokens = torch.randint(0, c["vocab"], (c["rows"], c["n_tok"]), device="cuda", generator=gen)
     tokens[:, :1] = at[:, :1]
-    s = {"case": c, "logits": wide.to(DTYPES[c["dtype"]])[:, :c["vocab"]], "tokens": tokens.int()}
-    if own:
-        from free_ffn_activation_b200 import decode
-        s["ws"] = decode.logprobs_workspace(c["rows"], c["vocab"], c["top_k"])
-    return s
+    return {"case": c, "logits": wide.to(DTYPES[c["dtype"]])[:, :c["vocab"]], "tokens": tokens.int()}
 
 
 # ---------------------------------------------------------------------------
@@ -336,7 +332,7 @@ def _own_attend(s):
 
 def _own_score(s):
     from free_ffn_activation_b200 import decode
-    r = decode.logprobs(s["logits"], s["tokens"], top_k=s["case"]["top_k"], ws=s["ws"])
+    r = decode.logprobs(s["logits"], s["tokens"], top_k=s["case"]["top_k"])
     return _score_out(s, r.logp, r.entropy, r.top_ids, r.top_logp)
 
 
@@ -347,7 +343,7 @@ def _own_pages(s):
     if c["kind"] == "branch":
         decode.cache_reserve(cache, s["dst"], s["n_new"])
         for layer in range(c["layers"]):
-            decode.cache_append(cache, layer, s["dst"], s["cu"], c["draft"], s["k_new"][layer], s["v_new"][layer])
+            decode.cache_append(cache, layer, s["dst"], s["cu"], s["k_new"][layer], s["v_new"][layer])
         decode.cache_compact(cache, s["dst"], s["path"], s["n_path"])
     decode.cache_free(cache, s["dst"])
     return {k: s[k] for k in POOL}
