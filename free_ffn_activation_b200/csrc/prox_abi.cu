@@ -142,7 +142,7 @@ struct DevInfo {
 static DevInfo g_dev[64];
 static std::mutex g_dev_mu;
 
-static prox_status current_device(int *sms) {
+prox_status current_device(int *sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PROX_ECUDA;
     if (dev < 0 || dev >= 64) return PROX_EDEVICE;
@@ -792,6 +792,7 @@ PROX_API const char *prox_status_str(prox_status s) {
         case PROX_ECUDA: return "CUDA error";
         case PROX_ETIMEOUT: return "device-side wait timed out";
         case PROX_EDEVICE: return "current device is not compute capability 10.x (B200)";
+        case PROX_EDATA: return "device-side data out of range";
     }
     return "unknown status";
 }

@@ -214,6 +214,9 @@ cudaError_t launch_select_f32_abs(const float *v, long n, long rank,
                                   uint32_t *hist, uint32_t *scratch,
                                   float *tau_dev, cudaStream_t s);
 
+// compute-capability check of the current device and its SM count
+prox_status current_device(int *sms);
+
 // Raise a kernel's dynamic shared-memory limit to at least `smem` bytes on the
 // current device (the attribute is per device; set once per device and kernel,
 // thread-safe)

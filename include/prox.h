@@ -48,7 +48,8 @@ typedef enum prox_status {
     PROX_ENOMEM = 2,   /* caller's workspace smaller than required           */
     PROX_ECUDA = 3,    /* a CUDA runtime call or launch failed               */
     PROX_ETIMEOUT = 4, /* a bounded device-side wait gave up (status word)   */
-    PROX_EDEVICE = 5   /* current device is not compute capability 10.x      */
+    PROX_EDEVICE = 5,  /* current device is not compute capability 10.x      */
+    PROX_EDATA = 6     /* device-side data out of range (prox_cache_status)  */
 } prox_status;
 
 /*
