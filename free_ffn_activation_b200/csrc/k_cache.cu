@@ -270,11 +270,12 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
         const int d = entry_seq(c, dst, i), s = entry_seq(c, src, i);
         b.seq[i] = -1;
         b.cols[i] = 0;
-        if (d < 0 || s < 0) return -1;
+        if (d < 0) return -1;
         if (b.first[d] != i) {
             atomicOr(c.status, PROX_CACHE_BAD_SEQ);
             return -1;
         }
+        if (s < 0) return -1;
         if (c.length[d] != 0 || c.held[d] != 0) {
             atomicOr(c.status, PROX_CACHE_BAD_ARG);
             return -1;
