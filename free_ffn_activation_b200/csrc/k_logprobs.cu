@@ -62,11 +62,24 @@ struct Elem;
 template <>
 struct Elem<PROX_FP32> {
     static constexpr int N = 4, BYTES = 4;
+    static constexpr uint32_t kLow = 0xff800000u;  // -inf
+    static __device__ __forceinline__ float max_of(const uint4 (&v)[kUnroll]) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            m = max_nan(max_nan(max_nan(__uint_as_float(v[u].x), __uint_as_float(v[u].y)),
+                                max_nan(__uint_as_float(v[u].z), __uint_as_float(v[u].w))),
+                        m);
+        return m;
+    }
     static __device__ __forceinline__ void unpack(const uint4 &v, float (&f)[4]) {
         f[0] = __uint_as_float(v.x);
         f[1] = __uint_as_float(v.y);
         f[2] = __uint_as_float(v.z);
         f[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ float pick(const uint4 &v, int j) {
+        return __uint_as_float(j & 2 ? (j & 1 ? v.w : v.z) : (j & 1 ? v.y : v.x));
     }
     static __device__ __forceinline__ float load(const void *p, long i) {
         return static_cast<const float *>(p)[i];
@@ -75,6 +88,18 @@ struct Elem<PROX_FP32> {
 template <>
 struct Elem<PROX_BF16> {
     static constexpr int N = 8, BYTES = 2;
+    static constexpr uint32_t kLow = 0xff80ff80u;  // -inf
+    static __device__ __forceinline__ float max_of(const uint4 (&v)[kUnroll]) {
+        using P = __nv_bfloat162;  // two elements a comparison; NaN if either is
+        auto at = [](uint32_t w) { return *reinterpret_cast<const P *>(&w); };
+        P m = __hmax2_nan(__hmax2_nan(at(v[0].x), at(v[0].y)), __hmax2_nan(at(v[0].z), at(v[0].w)));
+#pragma unroll
+        for (int u = 1; u < kUnroll; ++u)
+            m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(at(v[u].x), at(v[u].y)),
+                                           __hmax2_nan(at(v[u].z), at(v[u].w))));
+        const float2 f = __bfloat1622float2(m);
+        return max_nan(f.x, f.y);
+    }
     static __device__ __forceinline__ void unpack(const uint4 &v, float (&f)[8]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -83,6 +108,10 @@ struct Elem<PROX_BF16> {
             f[2 * k + 1] = bf16hi(w[k]);
         }
     }
+    static __device__ __forceinline__ float pick(const uint4 &v, int j) {
+        const uint32_t w = j & 4 ? (j & 2 ? v.w : v.z) : (j & 2 ? v.y : v.x);
+        return j & 1 ? bf16hi(w) : bf16lo(w);
+    }
     static __device__ __forceinline__ float load(const void *p, long i) {
         return __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i] << 16);
     }
@@ -90,6 +119,18 @@ struct Elem<PROX_BF16> {
 template <>
 struct Elem<PROX_FP16> {
     static constexpr int N = 8, BYTES = 2;
+    static constexpr uint32_t kLow = 0xfc00fc00u;  // -inf
+    static __device__ __forceinline__ float max_of(const uint4 (&v)[kUnroll]) {
+        using P = __half2;  // two elements a comparison; NaN if either is
+        auto at = [](uint32_t w) { return *reinterpret_cast<const P *>(&w); };
+        P m = __hmax2_nan(__hmax2_nan(at(v[0].x), at(v[0].y)), __hmax2_nan(at(v[0].z), at(v[0].w)));
+#pragma unroll
+        for (int u = 1; u < kUnroll; ++u)
+            m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(at(v[u].x), at(v[u].y)),
+                                           __hmax2_nan(at(v[u].z), at(v[u].w))));
+        const float2 f = __half22float2(m);
+        return max_nan(f.x, f.y);
+    }
     static __device__ __forceinline__ void unpack(const uint4 &v, float (&f)[8]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -99,15 +140,19 @@ struct Elem<PROX_FP16> {
             f[2 * k + 1] = p.y;
         }
     }
+    static __device__ __forceinline__ float pick(const uint4 &v, int j) {
+        const uint32_t w = j & 4 ? (j & 2 ? v.w : v.z) : (j & 2 ? v.y : v.x);
+        return __half2float(__ushort_as_half((unsigned short)(j & 1 ? w >> 16 : w)));
+    }
     static __device__ __forceinline__ float load(const void *p, long i) {
         return __half2float(static_cast<const __half *>(p)[i]);
     }
 };
 
 struct Shared {
-    unsigned long long cand[kCand];                  // key << 32 | ~index
+    alignas(16) unsigned long long cand[kCand + 8];  // key << 32 | ~index
+    alignas(16) unsigned long long joined[kMaxSplit * kMaxTop + 8];  // all CTAs' (first CTA)
     unsigned long long best[kMaxTop];                // the CTA's top k, descending
-    unsigned long long joined[kMaxSplit * kMaxTop];  // all CTAs' (first CTA only)
     unsigned long long sorted[kMaxTop];
     float m[kWarps];
     double s0[kWarps], s1[kWarps];
@@ -115,18 +160,29 @@ struct Shared {
     double cta_s0, cta_s1;
     uint32_t warp_key[kWarps];
     int n_cand, n_best;
+    int lost;                                        // candidates did not fit
     unsigned long long floor;                        // k-th largest so far (0 = none yet)
     float lse_m;
     double log_s0;
 };
 
-// places of `count` distinct codes in descending order: the first `keep` go to out
-__device__ __forceinline__ void select_top(const unsigned long long *in, int count, int keep,
+// places of `count` distinct codes in descending order: the first `keep` go to
+// out. `in` has room for 8 codes more, which are cleared here (0 is no code).
+// All threads; starts with a barrier.
+__device__ __forceinline__ void select_top(unsigned long long *in, int count, int keep,
                                            unsigned long long *out) {
+    if (threadIdx.x < 8) in[count + threadIdx.x] = 0;
+    __syncthreads();
     for (int t = threadIdx.x; t < count; t += kThreads) {
         const unsigned long long mine = in[t];
         int rank = 0;
-        for (int i = 0; i < count; ++i) rank += in[i] > mine;
+        for (int i = 0; i < count; i += 8) {
+            ulonglong2 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const ulonglong2 *>(in + i + 2 * u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) rank += (v[u].x > mine) + (v[u].y > mine);
+        }
         if (rank < keep) out[rank] = mine;
     }
 }
@@ -136,11 +192,12 @@ __device__ __forceinline__ void select_top(const unsigned long long *in, int cou
 __device__ void condense(Shared &sh, int k) {
     __syncthreads();
     const int count = min(sh.n_cand, kCand);
-    select_top(sh.cand, count, k, sh.best);
+    select_top(sh.cand, count, k, sh.best);  // (its barrier: all have read n_cand)
     __syncthreads();
     const int keep = min(count, k);
     if (threadIdx.x < keep) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
     if (threadIdx.x == 0) {
+        if (sh.n_cand > kCand) sh.lost = 1;
         sh.n_cand = keep;
         if (keep == k) sh.floor = sh.best[k - 1];
     }
@@ -160,53 +217,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a, i
     pdl_launch();
     const unsigned char *base =
         static_cast<const unsigned char *>(a.logits) + row * a.stride * E::BYTES;
-    // vector v covers the row's elements v * N - off .. + N - 1; the first and
-    // the last one may reach out of the row
+    // 16-byte vector v covers the row's elements v * N - off .. + N - 1; those
+    // that lie in the row as a whole are dealt out, the rest (fewer than 2 N
+    // elements at the row's ends) goes to the first CTA's first threads
     const int off = (int)((reinterpret_cast<uintptr_t>(base) & 15u) / E::BYTES);
     const uint4 *vec = reinterpret_cast<const uint4 *>(base - off * E::BYTES);
-    const int nvec = (a.vocab + off + N - 1) / N;
-    const int per = (nvec + split - 1) / split;
-    const int v0 = min(rank * per, nvec), v1 = min(v0 + per, nvec);
-    if (TOP && tid == 0) {
-        sh.n_cand = 0;
-        sh.floor = 0;
-    }
-
-    auto fetch = [&](int v) {
-        const long e0 = (long)v * N - off;
-        if (e0 >= 0 && e0 + N <= a.vocab) return __ldcs(vec + v);
-        float f[N];
-        uint4 r;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            f[j] = e0 + j >= 0 && e0 + j < a.vocab ? E::load(base, e0 + j) : -INFINITY;
-        if constexpr (DT == PROX_FP32) {
-            r = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                           __float_as_uint(f[3]));
-        } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (DT == PROX_BF16) {
-                    w[j] = (__float_as_uint(f[2 * j]) >> 16) |
-                           (__float_as_uint(f[2 * j + 1]) & 0xffff0000u);
-                } else {
-                    const __half2 h = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
-                    w[j] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-            }
-            r = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        return r;
-    };
+    const int first = off ? 1 : 0, last = (int)(((long)a.vocab + off) / N);
+    const int nvec = max(last - first, 0), per = (nvec + split - 1) / split;
+    const int v0 = first + min(rank * per, nvec), v1 = first + min((rank + 1) * per, nvec);
+    const int k = a.top_k;
 
     // a finite start, so that z is never inf - inf where nothing was seen yet
     float m = -FLT_MAX, s0 = 0.f, s1 = 0.f;
-    // one vector into the running sums (s1 in units of log2); returns its maximum
-    auto take = [&](const float (&x)[N]) {
-        float vm = x[0];
-#pragma unroll
-        for (int j = 1; j < N; ++j) vm = max_nan(vm, x[j]);
+    // makes vm's maximum the running one (s1 in units of log2)
+    auto raise_to = [&](float vm) {
         if (!(vm <= m)) {  // larger, or NaN
             const float nm = max_nan(m, vm);
             const float z = (m - nm) * kLog2e, r = ex2(z);
@@ -215,111 +239,172 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a, i
             s0 *= r;
             m = nm;
         }
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            // -inf and far values: e^z is 0, and z e^z must be too
-            const float z = max_nan((x[j] - m) * kLog2e, -1e30f);
-            const float e = ex2(z);
-            s0 += e;
-            s1 = fmaf(e, z, s1);
+    };
+    auto add = [&](float x) {
+        // -inf and far values: e^z is 0, and z e^z must be too
+        const float z = max_nan((x - m) * kLog2e, -1e30f);
+        const float e = ex2(z);
+        s0 += e;
+        s1 = fmaf(e, z, s1);
+    };
+    auto offer = [&](float x, long i, unsigned long long fl) {
+        const unsigned long long code =
+            ((unsigned long long)key_of(x) << 32) | (uint32_t)~(uint32_t)i;
+        if (code > fl) {  // (the floor itself is in already)
+            const int at = atomicAdd(&sh.n_cand, 1);
+            if (at < kCand) sh.cand[at] = code;
         }
-        return vm;
     };
 
-    if constexpr (TOP) __syncthreads();
-    const int k = a.top_k;
-    uint4 cur[kUnroll];
-    const int step = kThreads * kUnroll;
-    auto fetch_all = [&](int v) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            cur[u] = v + u * kThreads + tid < v1 ? fetch(v + u * kThreads + tid) : uint4{};
-    };
-    fetch_all(v0);
-    for (int v = v0; v < v1; v += step) {
-        uint4 now[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) now[u] = cur[u];
-        if (v + step < v1) fetch_all(v + step);
-        float vmax[kUnroll];
+    if constexpr (TOP) {
+        if (tid == 0) {
+            sh.n_cand = 0;
+            sh.floor = 0;
+            sh.lost = 0;
+        }
+        __syncthreads();
+    }
+    if (rank == 0 && tid < 2 * N) {
+        const long head = min((long)(off ? N - off : 0), (long)a.vocab);
+        const long tail = max(head, (long)last * N - off);
+        const long i = tid < N ? tid : tail + tid - N;
+        if (tid < N ? i < head : i < a.vocab) {
+            const float x = E::load(base, i);
+            raise_to(x);
+            add(x);
+            if constexpr (TOP) offer(x, i, 0);
+        }
+    }
+
+    constexpr int kStep = kThreads * kUnroll;
+    uint4 next[kUnroll];
+    auto fetch = [&](int v) {  // vectors behind the CTA's last one: -inf
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            vmax[u] = -INFINITY;
-            if (v + u * kThreads + tid < v1) {
-                float x[N];
-                E::unpack(now[u], x);
-                vmax[u] = take(x);
-            }
+            next[u] = make_uint4(E::kLow, E::kLow, E::kLow, E::kLow);
+            if (v + u * kThreads < v1) next[u] = __ldcs(vec + v + u * kThreads);
+        }
+    };
+    unsigned long long fl = 0;
+    float flv = key_value(0);  // NaN: nothing is below it
+    int steps = 0, refresh = 1;
+    fetch(v0 + tid);
+#pragma unroll 2
+    for (int vb = v0; vb < v1; vb += kStep) {
+        const int v = vb + tid;
+        uint4 cur[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) cur[u] = next[u];
+        if (vb + kStep < v1) fetch(v + kStep);
+        const float vmax = E::max_of(cur);
+        raise_to(vmax);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float x[N];
+            E::unpack(cur[u], x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) add(x[j]);
         }
         if constexpr (TOP) {
-            if (v == v0) {
+            if (steps == 0) {
                 // A first floor: of W full warps, each has r lanes whose maximum
                 // is at least its r-th largest; with r W >= k the smallest of
                 // these values has k elements at or above it.
                 const int full = min(kWarps, (v1 - v0) / 32);
                 const int r = full ? (k + full - 1) / full : 33;
-                uint32_t key = 0;
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u)
-                    if (v + u * kThreads + tid < v1) key = max(key, key_of(vmax[u]));
-                uint32_t rth = 0;
                 if (r <= 32) {
+                    uint32_t key = key_of(vmax), rth = 0;
                     for (int i = 0; i < r; ++i) {
                         rth = __reduce_max_sync(0xffffffffu, key);
                         const unsigned who = __ballot_sync(0xffffffffu, key == rth);
                         if (lane == __ffs(who) - 1) key = 0;
                     }
+                    if (lane == 0) sh.warp_key[wid] = wid < full ? rth : 0xffffffffu;
+                    __syncthreads();
+                    uint32_t lo = sh.warp_key[lane % kWarps];
+                    lo = __reduce_min_sync(0xffffffffu, lo);
+                    // below any index: elements of the floor's value are candidates
+                    fl = (unsigned long long)lo << 32;
+                    flv = key_value(lo);
                 }
-                if (lane == 0) sh.warp_key[wid] = wid < full ? rth : 0xffffffffu;
-                __syncthreads();
-                if (tid == 0 && r <= 32) {
-                    uint32_t lo = 0xffffffffu;
-                    for (int w = 0; w < kWarps; ++w) lo = min(lo, sh.warp_key[w]);
-                    // any index: elements equal to the floor's value stay candidates
-                    sh.floor = (unsigned long long)lo << 32;
-                }
-                __syncthreads();
             }
-            // candidates of this step; a step that does not fit is taken in
-            // several rounds, each of which raises the floor
-            unsigned pending = 0xffffffffu;
-            for (;;) {
-                const unsigned long long fl = sh.floor;
-                const float flv = key_value((uint32_t)(fl >> 32));
-                bool more = false;
+            if (!(vmax < flv)) {
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int vi = v + u * kThreads + tid;
-                    // (a floor of 0 is no floor: its value reads as NaN)
-                    if (vi >= v1 || vmax[u] < flv) continue;
+                    if (v + u * kThreads >= v1) continue;
                     float x[N];
-                    E::unpack(now[u], x);
+                    E::unpack(cur[u], x);
+                    const long i = (long)(v + u * kThreads) * N - off;
+                    unsigned hits = 0;
 #pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        const long e = (long)vi * N - off + j;
-                        const unsigned bit = 1u << (u * N + j);
-                        if (!(pending & bit) || e < 0 || e >= a.vocab) continue;
-                        const unsigned long long code =
-                            ((unsigned long long)key_of(x[j]) << 32) | (uint32_t)~(uint32_t)e;
-                        if (code <= fl) {  // (the floor itself is in already)
-                            pending &= ~bit;
-                            continue;
-                        }
-                        const int at = atomicAdd(&sh.n_cand, 1);
-                        if (at < kCand) {
-                            sh.cand[at] = code;
-                            pending &= ~bit;
-                        } else {
-                            more = true;
-                        }
+                    for (int j = 0; j < N; ++j) hits |= x[j] < flv ? 0u : 1u << j;
+                    while (hits) {
+                        const int j = __ffs(hits) - 1;
+                        hits &= hits - 1;
+                        offer(E::pick(cur[u], j), i + j, fl);
                     }
                 }
-                more = __syncthreads_or(more);
-                if (!more) break;
-                condense(sh, k);
             }
-            if (sh.n_cand > 2 * k + 128) condense(sh, k);  // (uniform: after the barrier)
+            // the floor is raised after steps 1, 4, 16, ...: of n elements
+            // about k ln 4 pass the floor of the first n / 4
+            if (++steps == refresh) {
+                refresh *= 4;
+                condense(sh, k);
+                if (sh.floor) {
+                    fl = sh.floor;
+                    flv = key_value((uint32_t)(fl >> 32));
+                }
+            }
+        }
+    }
+    if constexpr (TOP) {
+        condense(sh, k);
+        if (sh.lost) {
+            // More candidates at once than there is room for (rising rows): the
+            // row is read again, a vector a thread at a time, in rounds that each
+            // take what fits and raise the floor. (What was kept is a part of the
+            // row; all of it is offered again except what the floor rules out.)
             __syncthreads();
+            if (tid == 0) sh.n_cand = 0;
+            fl = 0;
+            __syncthreads();
+            if (rank == 0 && tid < 2 * N) {
+                const long head = min((long)(off ? N - off : 0), (long)a.vocab);
+                const long tail = max(head, (long)last * N - off);
+                const long i = tid < N ? tid : tail + tid - N;
+                if (tid < N ? i < head : i < a.vocab) offer(E::load(base, i), i, 0);
+            }
+            __syncthreads();  // (these are offered once: before the room fills)
+            for (int vb = v0; vb < v1; vb += kThreads) {
+                const int v = vb + tid;
+                unsigned pending = v < v1 ? (1u << N) - 1u : 0u;
+                float x[N] = {};
+                if (v < v1) E::unpack(vec[v], x);
+                for (;;) {
+                    bool more = false;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        if (!(pending >> j & 1)) continue;
+                        const unsigned long long code =
+                            ((unsigned long long)key_of(x[j]) << 32) |
+                            (uint32_t)~(uint32_t)((long)v * N - off + j);
+                        const int at = code > fl ? atomicAdd(&sh.n_cand, 1) : 0;
+                        if (code > fl && at < kCand) sh.cand[at] = code;
+                        if (code <= fl || at < kCand)
+                            pending &= ~(1u << j);
+                        else
+                            more = true;
+                    }
+                    more = __syncthreads_or(more);
+                    if (more || sh.n_cand > kCand / 2) {
+                        condense(sh, k);
+                        if (sh.n_cand == k) fl = sh.cand[k - 1];
+                    }
+                    __syncthreads();
+                    if (!more) break;
+                }
+            }
+            condense(sh, k);
         }
     }
 
@@ -341,7 +426,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a, i
             sh.s1[wid] = d1;
         }
     }
-    if constexpr (TOP) condense(sh, k);
     __syncthreads();
     if (tid == 0) {
         float M = sh.m[0];
@@ -393,7 +477,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a, i
                 if (tid < c) sh.joined[found + tid] = o->best[tid];
                 found += c;
             }
-            __syncthreads();
             select_top(sh.joined, found, k, sh.sorted);
         }
     }

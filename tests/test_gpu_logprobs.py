@@ -57,6 +57,19 @@ def test_equal_values_go_by_index(gpu):
         run(x, top_k=64)
 
 
+def test_row_ends_of_equal_values_are_not_lost(gpu):
+    """The elements before the first and behind the last whole vector count
+    even when every element of the row is a candidate."""
+    for dtype in TYPES:
+        x = torch.ones((3000, 9001), device=gpu, dtype=dtype)
+        for _ in range(5):
+            got = D.logprobs(x, top_k=9)
+            assert (got.top_ids == torch.arange(9, device=gpu)).all()
+        x[:, -3:] = 2.0
+        got = D.logprobs(x, top_k=5)
+        assert (got.top_ids == torch.tensor([8998, 8999, 9000, 0, 1], device=gpu)).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_orders_that_fill_the_candidates(gpu, dtype):
     """Ascending rows make every element a candidate when it is met."""
