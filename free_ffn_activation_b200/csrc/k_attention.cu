@@ -19,139 +19,19 @@
 // with mma.sync m16n8k16 (bf16 or fp16, fp32 sums): up to 64 rows the tensor
 // pipes keep up with the memory, and a warp's registers carry a tile of
 // scores straight into the second product.
-#include "decode_internal.cuh"
+#include "attention.cuh"
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
+#include <type_traits>
 
 namespace prox {
 namespace {
 
 constexpr int kKT = 64;             // keys of a tile
-constexpr int kGroup = 256;         // sequences of one launch
 constexpr int kWarps = 4;           // computing warps
 constexpr int kThreads = 32 * kWarps + 32;
 constexpr int kMaxStages = 8;
-constexpr int kNone = (int)0x80000000;   // no page to load
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// the line of tiles of one launch: entry i's tiles are pre[i] .. pre[i+1] - 1
-struct Line {
-    long long pre[kGroup + 1];
-    int seq[kGroup], len[kGroup], tot[kGroup];   // committed, and with drafted, tokens
-    int row0[kGroup], rows[kGroup];              // query rows
-};
-
-__device__ __forceinline__ int key_tiles(int tot) { return tot > 0 ? (tot + kKT - 1) / kKT : 1; }
-
-// all threads; ROWS: rows of a row tile. Flags are raised by one CTA only.
-__device__ void build_line(Line &ln, const AttnArgs &a, int ROWS, bool flag) {
-    const prox_cache &c = a.cache;
-    const int G = a.n_heads / c.n_kv_heads;
-    for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
-        const int c0 = a.cu_q[i], c1 = a.cu_q[i + 1], s = a.seqs[i];
-        const int r0 = min(max(c0, 0), a.rows);
-        const int r1 = min(max(c1, r0), min(a.rows, r0 + a.max_q));
-        int len = 0, tot = 0;
-        uint32_t bad = r0 != c0 || r1 != c1 ? PROX_CACHE_BAD_ARG : 0u;
-        if (s >= 0 && s < c.max_seqs) {
-            const int held0 = c.held[s], len0 = c.length[s];
-            const int held = min(max(held0, 0), c.max_pages);
-            const int room = held * c.page_size;
-            len = min(max(len0, 0), room);
-            tot = min(len + (r1 - r0), room);
-            if (held != held0 || len != len0) bad |= PROX_CACHE_BAD_STATE;
-            if (tot != len + (r1 - r0)) bad |= PROX_CACHE_FULL;
-        } else if (s != -1) {
-            bad |= PROX_CACHE_BAD_SEQ;
-        }
-        if (bad && flag) atomicOr(c.status, bad);
-        ln.seq[i] = s;
-        ln.len[i] = len;
-        ln.tot[i] = tot;
-        ln.row0[i] = r0;
-        ln.rows[i] = r1 - r0;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        long long at = 0;
-        for (int b = 0; b < a.n; b += 32) {
-            const int i = b + lane;
-            long long x = 0;
-            if (i < a.n)
-                x = (long long)c.n_kv_heads * ((ln.rows[i] * G + ROWS - 1) / ROWS) *
-                    key_tiles(ln.tot[i]);
-            const long long own = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            if (i < a.n) ln.pre[i] = at + x - own;
-            at += __shfl_sync(0xffffffffu, x, 31);
-        }
-        if (lane == 0) ln.pre[a.n] = at;
-    }
-    __syncthreads();
-}
-
-// tiles of a CTA's run
-__device__ __forceinline__ long long run_length(const Line &ln, int n, int grid) {
-    return max((ln.pre[n] + grid - 1) / grid, 1LL);
-}
-
-// last entry whose tiles begin at or before pos (pos < pre[n])
-__device__ __forceinline__ int entry_at(const Line &ln, int n, long long pos) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (ln.pre[mid] <= pos)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return lo;
-}
-
-// one stretch of a CTA's run: tiles tile0 .. tile0 + n_tiles - 1 of a unit
-struct Stretch {
-    int b, head, row_tile, tile0, n_tiles, all_tiles;
-};
-__device__ __forceinline__ Stretch stretch_at(const Line &ln, const AttnArgs &a, int ROWS,
-                                              long long pos, long long end) {
-    Stretch s;
-    s.b = entry_at(ln, a.n, pos);
-    const int G = a.n_heads / a.cache.n_kv_heads;
-    const int rt = (ln.rows[s.b] * G + ROWS - 1) / ROWS;
-    s.all_tiles = key_tiles(ln.tot[s.b]);
-    const long long local = pos - ln.pre[s.b];
-    const int unit = (int)(local / s.all_tiles);
-    s.tile0 = (int)(local - (long long)unit * s.all_tiles);
-    s.head = unit / rt;
-    s.row_tile = unit - s.head * rt;
-    s.n_tiles = (int)min((long long)(s.all_tiles - s.tile0), end - pos);
-    return s;
-}
-
-// 2-D tensor-map box global -> shared, completing on an mbarrier
-__device__ __forceinline__ void box_g2s(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                        uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
-        : "memory");
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -183,56 +63,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// two fp32 to packed bf16 / fp16 (round to nearest even), a in the low half
-template <int DT>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    if constexpr (DT == PROX_BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-}
-template <int DT>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-    if constexpr (DT == PROX_BF16)
-        return make_float2(bf16lo(w), bf16hi(w));
-    else
-        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-// a packed pair holds an infinity or NaN (exponent bits all set)
-template <int DT>
-__device__ __forceinline__ bool non_finite2(uint32_t w) {
-    constexpr uint32_t E = DT == PROX_BF16 ? 0x7f80u : 0x7c00u;
-    return (w & E) == E || (w & (E << 16)) == (E << 16);
-}
-
-// the low n bits set, any n
-__device__ __forceinline__ uint64_t low_bits(int n) {
-    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
-}
-
-// which of the 64 keys from position w0 on row `t` of a sequence sees (bits
-// of keys behind the last one are cut off by the caller)
-__device__ __forceinline__ uint64_t seen_bits(const uint64_t *tree, int words, int len, int t,
-                                              int w0) {
-    const int c = len - w0;  // committed keys in the window
-    if (!tree) return low_bits(c + t + 1);
-    uint64_t bits = low_bits(c);
-    if (c >= 64) return bits;
-    if (c > 0) return bits | tree[0] << c;
-    const int w = -c >> 6, o = -c & 63;
-    if (w < words) bits |= tree[w] >> o;
-    if (o && w + 1 < words) bits |= tree[w + 1] << (64 - o);
-    return bits;
-}
-
 template <int D, int RG>
 struct Cfg {
     static constexpr int KG = kWarps / RG;        // key groups
     static constexpr int WK = kKT / KG;           // keys of a tile one warp takes
     static constexpr int ROWS = 16 * RG;
+    static constexpr TileShape TS{ROWS, kKT};
     static constexpr int NST = D == 128 ? 3 : 6;  // ring stages
     static constexpr int HALF = kKT * 128;        // bytes of 64 elements of a tile's rows
     static constexpr int TILE = HALF * (D / 64);  // bytes of a tile of k (or v)
@@ -290,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
     }
     pdl_wait();
     pdl_launch();
-    build_line(ln, a, ROWS, blockIdx.x == 0);  // (its barriers cover the mbarriers too)
+    build_line(ln, a, C::TS, blockIdx.x == 0);  // (its barriers cover the mbarriers too)
     const long long run = run_length(ln, a.n, a.grid);
     const long long begin = blockIdx.x * run, end = min(begin + run, ln.pre[a.n]);
     if (begin >= end) return;
@@ -306,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
         bool live = true;
         int it = 0;
         for (long long pos = begin; pos < end;) {
-            const Stretch st = stretch_at(ln, a, ROWS, pos, end);
+            const Stretch st = stretch_at(ln, a, C::TS, pos, end);
             pos += st.n_tiles;
             const int tot = ln.tot[st.b];
             const int32_t *table = c.page_table + (size_t)max(ln.seq[st.b], 0) * c.max_pages;
@@ -361,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
     bool live = true;
     int it = 0;
     for (long long pos = begin; pos < end;) {
-        const Stretch st = stretch_at(ln, a, ROWS, pos, end);
+        const Stretch st = stretch_at(ln, a, C::TS, pos, end);
         const bool first = pos == begin;
         pos += st.n_tiles;
         const int len = ln.len[st.b], tot = ln.tot[st.b];
@@ -646,14 +482,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
                                                              : (m[e] + log2f(l[e])) * kLn2;
                 }
             } else {
-                float *part = a.part + (size_t)(blockIdx.x * 2 + (first ? 0 : 1)) * ROWS * (D + 2);
-                float *pm = part + ROWS * D;
+                float *part = piece(a, blockIdx.x, first, D, ROWS), *pm = part + ROWS * D;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = rg * 16 + g + 8 * e;
 #pragma unroll
                     for (int d = 0; d < DB; ++d)
-                        *reinterpret_cast<float2 *>(part + (size_t)r * D + d * 8 + tg * 2) =
+                        *reinterpret_cast<float2 *>(
+                            part + ((size_t)(d * 2 + (tg >> 1)) * ROWS + r) * 4 + (tg & 1) * 2) =
                             make_float2(o[d][2 * e], o[d][2 * e + 1]);
                     if (tg == 0) {
                         pm[r] = m[e];
@@ -666,73 +502,83 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
     }
 }
 
-// Joins the pieces of units that were cut: one warp an output row, the pieces
-// in the order of the line.
+// Joins the pieces of units that were cut, in the order of the line. One CTA
+// takes 32 rows of a unit: lanes are rows, a warp has 1/8 of the columns, so a
+// piece is read in runs of 512 bytes and each warp has several in flight.
 template <int D, int DT>
-__global__ void __launch_bounds__(256) k_attention_join(const __grid_constant__ AttnArgs a, int ROWS) {
+__global__ void __launch_bounds__(256)
+    k_attention_join(const __grid_constant__ AttnArgs a, TileShape ts, int max_rows) {
     __shared__ Line ln;
+    // The line depends on the call's inputs alone, which were there before the
+    // main kernel let this one start; its pieces come after the wait.
+    build_line(ln, a, ts, false);
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int groups = (max_rows + 31) / 32, heads = a.cache.n_kv_heads;
+    const int grp = blockIdx.x % groups, bh = blockIdx.x / groups;
+    const int head = bh % heads, b = bh / heads;
+    const int G = a.n_heads / heads, n_rows = ln.rows[b] * G;
+    const int row0 = grp * 32, r = row0 + lane;
+    if (row0 < n_rows) {
+        const int rt = (n_rows + ts.rows - 1) / ts.rows, kt = key_tiles(ln.tot[b], ts);
+        const long long run = run_length(ln, a.n, a.grid);
+        const long long u0 = ln.pre[b] + ((long long)head * rt + row0 / ts.rows) * kt, u1 = u0 + kt;
+        const long long c0 = u0 / run, c1 = (u1 - 1) / run;
+        if (c0 != c1) {  // else written by its CTA
+            pdl_wait();
+            const int rr = r % ts.rows;
+            // (rows behind the last one read their neighbours' place in the piece)
+            auto at = [&](long long c) { return piece(a, c, c * run >= u0, D, ts.rows); };
+            float M = -INFINITY;
+#pragma unroll 8
+            for (long long c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(at(c) + ts.rows * D + rr));
+            const float mu = M == -INFINITY ? 0.f : M;
+            constexpr int V = D / 32;  // float4 columns of a warp
+            float o[V][4] = {}, l = 0.f;
+#pragma unroll 4
+            for (long long c = c0; c <= c1; ++c) {
+                const float *p = at(c);
+                const float f = ex2(__ldcg(p + ts.rows * D + rr) - mu);
+                l += f * __ldcg(p + ts.rows * (D + 1) + rr);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float4 x =
+                        __ldcg(reinterpret_cast<const float4 *>(p) + (size_t)(wid * V + v) * ts.rows + rr);
+                    o[v][0] = fmaf(f, x.x, o[v][0]);
+                    o[v][1] = fmaf(f, x.y, o[v][1]);
+                    o[v][2] = fmaf(f, x.z, o[v][2]);
+                    o[v][3] = fmaf(f, x.w, o[v][3]);
+                }
+            }
+            if (r < n_rows) {
+                const int t = r / G, hq = head * G + r - t * G;
+                const size_t row = ln.row0[b] + t;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                uint32_t w[V * 2];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    w[2 * v] = pack2<DT>(o[v][0] * inv, o[v][1] * inv);
+                    w[2 * v + 1] = pack2<DT>(o[v][2] * inv, o[v][3] * inv);
+                }
+                uint16_t *op = a.out + row * a.out_stride + (size_t)hq * D + wid * V * 4;
+#pragma unroll
+                for (int v = 0; v < V; v += 2)
+                    *reinterpret_cast<uint4 *>(op + v * 4) =
+                        make_uint4(w[2 * v], w[2 * v + 1], w[2 * v + 2], w[2 * v + 3]);
+                if (a.lse && wid == 0)
+                    a.lse[row * a.n_heads + hq] =
+                        M == -INFINITY && l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+            }
+        }
+    }
+    // every CTA waits before it ends: what follows this kernel in the stream
+    // may count on the main kernel being done
     pdl_wait();
     pdl_launch();
-    build_line(ln, a, ROWS, false);
-    const long long id = (long long)blockIdx.x * 8 + wid;
-    const int row = (int)(id / a.n_heads), head = (int)(id - (long long)row * a.n_heads);
-    if (row >= a.rows) return;
-    int b = -1;
-    for (int i0 = 0; i0 < a.n; i0 += 32) {
-        const int i = i0 + lane;
-        const bool in = i < a.n && row >= ln.row0[i] && row < ln.row0[i] + ln.rows[i];
-        const unsigned who = __ballot_sync(0xffffffffu, in);
-        if (who && b < 0) b = i0 + __ffs(who) - 1;
-    }
-    if (b < 0) return;
-    const int G = a.n_heads / a.cache.n_kv_heads;
-    const int r = (row - ln.row0[b]) * G + head % G;
-    const int rt = (ln.rows[b] * G + ROWS - 1) / ROWS, kt = key_tiles(ln.tot[b]);
-    const long long run = run_length(ln, a.n, a.grid);
-    const long long u0 = ln.pre[b] + ((long long)(head / G) * rt + r / ROWS) * kt, u1 = u0 + kt;
-    const long long c0 = u0 / run, c1 = (u1 - 1) / run;
-    if (c0 == c1) return;  // written by its CTA
-    const int rr = r % ROWS;
-    constexpr int V = D / 32;
-    float o[V] = {}, m = -INFINITY, l = 0.f;
-    for (long long cta = c0; cta <= c1; ++cta) {
-        const float *part = a.part + (size_t)(cta * 2 + (cta * run >= u0 ? 0 : 1)) * ROWS * (D + 2);
-        const float pm = part[ROWS * D + rr], pl = part[ROWS * D + ROWS + rr];
-        float x[V];
-        if constexpr (V == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(part + (size_t)rr * D + lane * 4);
-            x[0] = v.x;
-            x[1] = v.y;
-            x[2] = v.z;
-            x[3] = v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(part + (size_t)rr * D + lane * 2);
-            x[0] = v.x;
-            x[1] = v.y;
-        }
-        const float nm = fmaxf(m, pm), mu = nm == -INFINITY ? 0.f : nm;
-        const float f0 = ex2(m - mu), f1 = ex2(pm - mu);
-        l = l * f0 + pl * f1;
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = o[k] * f0 + x[k] * f1;
-        m = nm;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t *op = a.out + (size_t)row * a.out_stride + (size_t)head * D + lane * V;
-    if constexpr (V == 4)
-        *reinterpret_cast<uint2 *>(op) =
-            make_uint2(pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(op) = pack2<DT>(o[0] * inv, o[1] * inv);
-    if (a.lse && lane == 0)
-        a.lse[(size_t)row * a.n_heads + head] =
-            m == -INFINITY && l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-template <typename K>
-cudaError_t launch(K kern, int grid, int block, size_t smem, cudaStream_t s, const AttnArgs &a,
-                   int rows = -1) {
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), int grid, int block, size_t smem, cudaStream_t s,
+                   const A &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
@@ -743,10 +589,7 @@ cudaError_t launch(K kern, int grid, int block, size_t smem, cudaStream_t s, con
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if constexpr (std::is_same<K, void (*)(const AttnArgs, int)>::value)
-        return cudaLaunchKernelEx(&cfg, kern, a, rows);
-    else
-        return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int D, int DT, int RG>
@@ -757,19 +600,30 @@ cudaError_t run_main(const AttnArgs &a, cudaStream_t s) {
     return launch(k_attention<D, DT, RG>, a.grid, kThreads, smem, s, a);
 }
 
-template <int D, int DT>
-cudaError_t run_typed(const AttnArgs &a, int row_groups, cudaStream_t s) {
-    cudaError_t e = row_groups == 1   ? run_main<D, DT, 1>(a, s)
-                    : row_groups == 2 ? run_main<D, DT, 2>(a, s)
-                                      : run_main<D, DT, 4>(a, s);
-    if (e != cudaSuccess) return e;
-    const long long rows = ((long long)a.rows * a.n_heads + 7) / 8;
-    return launch(k_attention_join<D, DT>, (int)rows, 256, 0, s, a, 16 * row_groups);
+// How a call runs: row tiles of 16 to 64 rows on mma.sync, of 128 and 256 rows
+// on the tensor memory's MMA
+struct Plan {
+    TileShape ts;
+    int grid_per_sm;
+    bool tc;
+};
+Plan plan_of(int max_rows) {
+    if (max_rows <= 16) return {{16, kKT}, 2, false};
+    if (max_rows <= 32) return {{32, kKT}, 2, false};
+    if (max_rows <= 128) return {{128, 128}, 1, true};
+    return {{256, 128}, 1, true};
 }
 
-// rows of a row tile: the smallest of 16, 32 and 64 that holds all rows of a
-// key/value head
-int row_groups_of(int max_rows) { return max_rows <= 16 ? 1 : max_rows <= 32 ? 2 : 4; }
+template <int D, int DT>
+cudaError_t run_typed(const AttnArgs &a, const Plan &p, int max_rows, cudaStream_t s) {
+    cudaError_t e = p.tc              ? launch_attention_tc(a, p.ts.rows / 128, s)
+                    : p.ts.rows == 16 ? run_main<D, DT, 1>(a, s)
+                                      : run_main<D, DT, 2>(a, s);
+    if (e != cudaSuccess) return e;
+    const int groups = (max_rows + 31) / 32;
+    return launch(k_attention_join<D, DT>, a.n * a.cache.n_kv_heads * groups, 256, 0, s, a, p.ts,
+                  max_rows);
+}
 
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -790,11 +644,11 @@ EncodeFn encode_fn() {
 }
 
 // boxes of 64 elements and up to one page's rows, 128-byte swizzled
-bool encode_rows(CUtensorMap *map, const prox_cache &c, const uint16_t *base) {
+bool encode_rows(CUtensorMap *map, const prox_cache &c, const uint16_t *base, int keys) {
     const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim,
                                 (cuuint64_t)c.n_pages * c.n_kv_heads * c.page_size};
     const cuuint64_t strides[1] = {(cuuint64_t)c.head_dim * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)(c.page_size < kKT ? c.page_size : kKT)};
+    const cuuint32_t box[2] = {64, (cuuint32_t)(c.page_size < keys ? c.page_size : keys)};
     const cuuint32_t ones[2] = {1, 1};
     EncodeFn fn = encode_fn();
     return fn && fn(map,
@@ -809,15 +663,17 @@ bool encode_rows(CUtensorMap *map, const prox_cache &c, const uint16_t *base) {
 }  // namespace
 
 size_t attention_part_bytes(int head_dim, int max_rows, int sms) {
-    return (size_t)sms * 2 * 2 * 16 * row_groups_of(max_rows) * (head_dim + 2) * sizeof(float);
+    const Plan p = plan_of(max_rows);
+    return (size_t)sms * p.grid_per_sm * 2 * piece_floats(head_dim, p.ts.rows) * sizeof(float);
 }
 
 cudaError_t launch_attention(AttnArgs &a, const uint16_t *k_layer, int max_rows, int sms,
                              cudaStream_t s) {
-    if (!encode_rows(&a.map_k, a.cache, k_layer) || !encode_rows(&a.map_v, a.cache, a.v_layer))
+    const Plan p = plan_of(max_rows);
+    if (!encode_rows(&a.map_k, a.cache, k_layer, p.ts.keys) ||
+        !encode_rows(&a.map_v, a.cache, a.v_layer, p.ts.keys))
         return cudaErrorInvalidValue;
-    a.grid = sms * 2;
-    const int rg = row_groups_of(max_rows);
+    a.grid = sms * p.grid_per_sm;
     const int32_t *seqs = a.seqs, *cu = a.cu_q;
     const int n = a.n;
     for (int at = 0; at < n; at += kGroup) {
@@ -826,11 +682,11 @@ cudaError_t launch_attention(AttnArgs &a, const uint16_t *k_layer, int max_rows,
         a.cu_q = cu + at;
         cudaError_t e;
         if (a.cache.head_dim == 128)
-            e = a.cache.dtype == PROX_BF16 ? run_typed<128, PROX_BF16>(a, rg, s)
-                                           : run_typed<128, PROX_FP16>(a, rg, s);
+            e = a.cache.dtype == PROX_BF16 ? run_typed<128, PROX_BF16>(a, p, max_rows, s)
+                                           : run_typed<128, PROX_FP16>(a, p, max_rows, s);
         else
-            e = a.cache.dtype == PROX_BF16 ? run_typed<64, PROX_BF16>(a, rg, s)
-                                           : run_typed<64, PROX_FP16>(a, rg, s);
+            e = a.cache.dtype == PROX_BF16 ? run_typed<64, PROX_BF16>(a, p, max_rows, s)
+                                           : run_typed<64, PROX_FP16>(a, p, max_rows, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

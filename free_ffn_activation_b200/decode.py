@@ -74,6 +74,11 @@ def _on(dev: torch.device):
     return _NONE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
+def _stream(dev: torch.device) -> int:
+    """The current stream's handle (without building a torch.cuda.Stream)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _ints(t: torch.Tensor, shape: tuple, dev: torch.device, name: str, dtype=torch.int32) -> int:
     """Pointer of a contiguous device list, checked."""
     if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
@@ -118,7 +123,7 @@ class PagedCache:
                     torch.empty(shape, dtype=dtype, device=dev), i32((max_seqs, max_pages)),
                     i32(max_seqs), i32(max_seqs), i32(n_pages), i32(n_pages), i32(1))
         with _on(dev):
-            P._check(_lib().prox_cache_init(self._ref, P._stream(dev)), "prox_cache_init")
+            P._check(_lib().prox_cache_init(self._ref, _stream(dev)), "prox_cache_init")
 
     @classmethod
     def from_tensors(cls, k, v, page_table, length, held, ref_count, free_list, n_free) -> "PagedCache":
@@ -165,7 +170,7 @@ def cache_reserve(cache: PagedCache, seqs: torch.Tensor, n_new: torch.Tensor,
     a = (n, _ints(seqs, (n,), dev, "seqs"), _ints(n_new, (n,), dev, "n_new"),
          None if ok is None else _ints(ok, (n,), dev, "ok", torch.uint8))
     with _on(dev):
-        P._check(_lib().prox_cache_reserve(cache._ref, *a, P._stream(dev)), "prox_cache_reserve")
+        P._check(_lib().prox_cache_reserve(cache._ref, *a, _stream(dev)), "prox_cache_reserve")
 
 
 def cache_append(cache: PagedCache, layer: int, seqs: torch.Tensor, cu_new: torch.Tensor,
@@ -181,7 +186,7 @@ def cache_append(cache: PagedCache, layer: int, seqs: torch.Tensor, cu_new: torc
     a = (layer, n, _ints(seqs, (n,), dev, "seqs"), _ints(cu_new, (n + 1,), dev, "cu_new"),
          k_new.shape[0], kp, ks, vp, vs)
     with _on(dev):
-        P._check(_lib().prox_cache_append(cache._ref, *a, P._stream(dev)), "prox_cache_append")
+        P._check(_lib().prox_cache_append(cache._ref, *a, _stream(dev)), "prox_cache_append")
 
 
 def cache_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, *, share: bool = True,
@@ -193,7 +198,7 @@ def cache_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, *, share
          None if ok is None else _ints(ok, (n,), dev, "ok", torch.uint8), cache._ws.data_ptr(),
          cache._ws.numel())
     with _on(dev):
-        P._check(_lib().prox_cache_fork(cache._ref, *a, P._stream(dev)), "prox_cache_fork")
+        P._check(_lib().prox_cache_fork(cache._ref, *a, _stream(dev)), "prox_cache_fork")
 
 
 def cache_compact(cache: PagedCache, seqs: torch.Tensor, path: torch.Tensor, n_path: torch.Tensor,
@@ -207,7 +212,7 @@ def cache_compact(cache: PagedCache, seqs: torch.Tensor, path: torch.Tensor, n_p
          path.shape[1], _ints(n_path, (n,), dev, "n_path"),
          None if ok is None else _ints(ok, (n,), dev, "ok", torch.uint8))
     with _on(dev):
-        P._check(_lib().prox_cache_compact(cache._ref, *a, P._stream(dev)), "prox_cache_compact")
+        P._check(_lib().prox_cache_compact(cache._ref, *a, _stream(dev)), "prox_cache_compact")
 
 
 def cache_free(cache: PagedCache, seqs: torch.Tensor) -> None:
@@ -215,14 +220,14 @@ def cache_free(cache: PagedCache, seqs: torch.Tensor) -> None:
     n, dev = seqs.numel(), cache.device
     p = _ints(seqs, (n,), dev, "seqs")
     with _on(dev):
-        P._check(_lib().prox_cache_free(cache._ref, n, p, P._stream(dev)), "prox_cache_free")
+        P._check(_lib().prox_cache_free(cache._ref, n, p, _stream(dev)), "prox_cache_free")
 
 
 def cache_status(cache: PagedCache) -> tuple[int, int]:
     """(status, CACHE_* bits) of the cache's status word; clears it."""
     flags = C.c_uint32()
     with _on(cache.device):
-        st = _lib().prox_cache_status(cache._ref, P._stream(cache.device), C.byref(flags))
+        st = _lib().prox_cache_status(cache._ref, _stream(cache.device), C.byref(flags))
     return st, flags.value
 
 
@@ -254,12 +259,12 @@ def tree_attention(cache: PagedCache, layer: int, q: torch.Tensor, seqs: torch.T
     qp, qs = _rows(q, heads, cache.head_dim, cache.dtype, dev, "q")
     rows = q.shape[0]
     if out is None:
-        out = torch.empty((rows, heads, cache.head_dim), dtype=cache.dtype, device=dev)
+        out = q.new_empty((rows, heads, cache.head_dim))
     elif out.shape != q.shape:
         raise ValueError(f"out must have shape {tuple(q.shape)}, got {tuple(out.shape)}")
     op, os_ = _rows(out, heads, cache.head_dim, cache.dtype, dev, "out")
     if lse is None:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
+        lse = q.new_empty((rows, heads), dtype=torch.float32)
     if ws is None:
         ws = attention_workspace(cache, max_q, heads)
     words = 0
@@ -271,7 +276,7 @@ def tree_attention(cache: PagedCache, layer: int, q: torch.Tensor, seqs: torch.T
          os_, _ints(lse, (rows, heads), dev, "lse", torch.float32),
          _ints(ws, (ws.numel(),), dev, "ws", torch.uint8), ws.numel())
     with _on(dev):
-        P._check(_lib().prox_tree_attention(cache._ref, *a, P._stream(dev)), "prox_tree_attention")
+        P._check(_lib().prox_tree_attention(cache._ref, *a, _stream(dev)), "prox_tree_attention")
     return out, lse
 
 
@@ -305,15 +310,16 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, *,
             tokens = tokens.unsqueeze(1)
         n_tok = tokens.shape[1] if tokens.dim() == 2 else -1
         tp = _ints(tokens, (rows, n_tok), dev, "tokens")
-    f32 = functools.partial(torch.empty, dtype=torch.float32, device=dev)
-    out = LogprobsOut(f32((rows, n_tok)) if n_tok else None, f32(rows),
-                      torch.empty((rows, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None,
-                      f32((rows, top_k)) if top_k > 0 else None)
+    f32, k = torch.float32, top_k > 0
+    out = LogprobsOut(logits.new_empty((rows, n_tok), dtype=f32) if n_tok else None,
+                      logits.new_empty((rows,), dtype=f32),
+                      logits.new_empty((rows, top_k), dtype=torch.int32) if k else None,
+                      logits.new_empty((rows, top_k), dtype=f32) if k else None)
     a = (rows, vocab, DTYPES[logits.dtype], logits.data_ptr(),
          logits.stride(0) if rows > 1 else vocab, tp if n_tok else None, n_tok, top_k,
          P._ptr(out.logp), out.entropy.data_ptr(), P._ptr(out.top_ids), P._ptr(out.top_logp))
     with _on(dev):
-        P._check(_lib().prox_logprobs(*a, P._stream(dev)), "prox_logprobs")
+        P._check(_lib().prox_logprobs(*a, _stream(dev)), "prox_logprobs")
     return out
 
 
