@@ -16,10 +16,7 @@ constexpr int kNone = (int)0x80000000;    // no page to load
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// shape of a kernel's tiles: rows of a row tile, keys of a key tile
-struct TileShape {
-    int rows, keys;
-};
+constexpr int kKT = 64;                   // keys of a tile
 
 #ifdef __CUDACC__
 
@@ -30,18 +27,17 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // the line of tiles of one launch: entry i's tiles are pre[i] .. pre[i+1] - 1
-struct Line {
-    long long pre[kGroup + 1];
+// (the host keeps a launch's tiles below 2^31)
+struct alignas(16) Line {
+    int pre[kGroup + 1];
     int seq[kGroup], len[kGroup], tot[kGroup];   // committed, and with drafted, tokens
     int row0[kGroup], rows[kGroup];              // query rows
 };
 
-__device__ __forceinline__ int key_tiles(int tot, TileShape ts) {
-    return tot > 0 ? (tot + ts.keys - 1) / ts.keys : 1;
-}
+__device__ __forceinline__ int key_tiles(int tot) { return tot > 0 ? (tot + kKT - 1) / kKT : 1; }
 
-// all threads; flags are raised by one CTA only
-__device__ inline void build_line(Line &ln, const AttnArgs &a, TileShape ts, bool flag) {
+// all threads; ROWS: rows of a row tile. Flags are raised by one CTA only.
+__device__ inline void build_line(Line &ln, const AttnArgs &a, int ROWS, bool flag) {
     const prox_cache &c = a.cache;
     const int G = a.n_heads / c.n_kv_heads;
     for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
@@ -71,17 +67,16 @@ __device__ inline void build_line(Line &ln, const AttnArgs &a, TileShape ts, boo
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        long long at = 0;
+        int at = 0;
         for (int b = 0; b < a.n; b += 32) {
             const int i = b + lane;
-            long long x = 0;
+            int x = 0;
             if (i < a.n)
-                x = (long long)c.n_kv_heads * ((ln.rows[i] * G + ts.rows - 1) / ts.rows) *
-                    key_tiles(ln.tot[i], ts);
-            const long long own = x;
+                x = c.n_kv_heads * ((ln.rows[i] * G + ROWS - 1) / ROWS) * key_tiles(ln.tot[i]);
+            const int own = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
             if (i < a.n) ln.pre[i] = at + x - own;
@@ -93,13 +88,19 @@ __device__ inline void build_line(Line &ln, const AttnArgs &a, TileShape ts, boo
 }
 
 // tiles of a CTA's run
-__device__ __forceinline__ long long run_length(const Line &ln, int n, int grid) {
-    return max((ln.pre[n] + grid - 1) / grid, 1LL);
+__device__ __forceinline__ int run_length(const Line &ln, int n, int grid) {
+    return max((int)(((unsigned)ln.pre[n] + grid - 1) / grid), 1);
 }
 
-// last entry whose tiles begin at or before pos (pos < pre[n])
-__device__ __forceinline__ int entry_at(const Line &ln, int n, long long pos) {
-    int lo = 0, hi = n - 1;
+// one stretch of a CTA's run: tiles tile0 .. tile0 + n_tiles - 1 of a unit
+struct Stretch {
+    int b, head, row_tile, tile0, n_tiles, all_tiles;
+};
+__device__ __forceinline__ Stretch stretch_at(const Line &ln, const AttnArgs &a, int ROWS, int pos,
+                                              int end) {
+    Stretch s;
+    // last entry whose tiles begin at or before pos (pos < pre[n])
+    int lo = 0, hi = a.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (ln.pre[mid] <= pos)
@@ -107,26 +108,16 @@ __device__ __forceinline__ int entry_at(const Line &ln, int n, long long pos) {
         else
             hi = mid - 1;
     }
-    return lo;
-}
-
-// one stretch of a CTA's run: tiles tile0 .. tile0 + n_tiles - 1 of a unit
-struct Stretch {
-    int b, head, row_tile, tile0, n_tiles, all_tiles;
-};
-__device__ __forceinline__ Stretch stretch_at(const Line &ln, const AttnArgs &a, TileShape ts,
-                                              long long pos, long long end) {
-    Stretch s;
-    s.b = entry_at(ln, a.n, pos);
+    s.b = lo;
     const int G = a.n_heads / a.cache.n_kv_heads;
-    const int rt = (ln.rows[s.b] * G + ts.rows - 1) / ts.rows;
-    s.all_tiles = key_tiles(ln.tot[s.b], ts);
-    const long long local = pos - ln.pre[s.b];
-    const int unit = (int)(local / s.all_tiles);
-    s.tile0 = (int)(local - (long long)unit * s.all_tiles);
+    const int rt = (ln.rows[s.b] * G + ROWS - 1) / ROWS;
+    s.all_tiles = key_tiles(ln.tot[s.b]);
+    const int local = pos - ln.pre[s.b];
+    const int unit = local / s.all_tiles;
+    s.tile0 = local - unit * s.all_tiles;
     s.head = unit / rt;
     s.row_tile = unit - s.head * rt;
-    s.n_tiles = (int)min((long long)(s.all_tiles - s.tile0), end - pos);
+    s.n_tiles = min(s.all_tiles - s.tile0, end - pos);
     return s;
 }
 
@@ -201,14 +192,13 @@ __device__ __forceinline__ uint64_t seen_bits(const uint64_t *tree, int words, i
 __host__ __device__ constexpr size_t piece_floats(int dim, int rows) {
     return (size_t)rows * (dim + 2);
 }
-__device__ __forceinline__ float *piece(const AttnArgs &a, long long cta, bool first, int dim,
-                                        int rows) {
+__device__ __forceinline__ float *piece(const AttnArgs &a, int cta, bool first, int dim, int rows) {
     return a.part + (size_t)(cta * 2 + (first ? 0 : 1)) * piece_floats(dim, rows);
 }
 
 #endif  // __CUDACC__
 
-// main kernels; the tile shape that launch_attention picked goes with them
+// the tensor-memory kernel with one or two row groups of 128 rows
 cudaError_t launch_attention_tc(const AttnArgs &a, int row_groups, cudaStream_t s);
 
 }  // namespace prox

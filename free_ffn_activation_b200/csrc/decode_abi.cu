@@ -167,6 +167,7 @@ PROX_API prox_status prox_tree_attention(const prox_cache *cache, int layer, int
         !heads_ok(cache, n_heads) || max_q < 1 || max_q > kMaxDraft ||
         (long long)rows * n_heads > 1ll << 31)
         return PROX_EINVAL;
+    const int max_rows = max_q * (n_heads / cache->n_kv_heads);
     if (!std::isfinite(scale) || !(scale > 0.f)) return PROX_EINVAL;
     if (tree && (tree_words < (max_q + 63) / 64 || tree_words > 1 << 20)) return PROX_EINVAL;
     if (n == 0 || rows == 0) return PROX_OK;
@@ -177,7 +178,7 @@ PROX_API prox_status prox_tree_attention(const prox_cache *cache, int layer, int
         return PROX_EINVAL;
     int sms;
     if ((ps = current_device(&sms)) != PROX_OK) return ps;
-    const int max_rows = max_q * (n_heads / cache->n_kv_heads);
+    if (!attention_fits(*cache, max_rows)) return PROX_EINVAL;
     if (ws_bytes < attention_part_bytes(cache->head_dim, max_rows, sms)) return PROX_ENOMEM;
     const size_t one = (size_t)cache->n_pages * cache->n_kv_heads * cache->page_size * cache->head_dim;
     AttnArgs a{};

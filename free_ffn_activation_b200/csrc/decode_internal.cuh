@@ -46,6 +46,8 @@ struct AttnArgs {
     int grid;                               // CTAs of the main kernel
     uint32_t wait_us;                       // wall-clock bound of each wait, microseconds
 };
+// whether a sequence's tiles can be numbered in 31 bits
+bool attention_fits(const prox_cache &c, int max_rows);
 size_t attention_part_bytes(int head_dim, int max_rows, int sms);
 cudaError_t launch_attention(AttnArgs &a, const uint16_t *k_layer, int max_rows, int sms,
                              cudaStream_t s);
@@ -87,6 +89,30 @@ __device__ __forceinline__ SeqState seq_state(const prox_cache &c, int s) {
 
 __device__ __forceinline__ bool page_ok(const prox_cache &c, int p) {
     return p >= 0 && p < c.n_pages;
+}
+
+// Bounded wait on the phase of `bar` with the given parity, for handovers of a
+// microsecond: tries without a sleep hint, and looks at the clock only now and
+// then. False once limit_us microseconds have passed.
+__device__ __forceinline__ bool mbar_spin(uint64_t *bar, uint32_t parity, uint32_t limit_us) {
+    const uint32_t addr = smem_addr(bar);
+    uint64_t t0 = 0;
+    for (uint32_t tries = 0;; ++tries) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((tries & 63u) == 63u) {
+            const uint64_t now = global_ns();
+            if (!t0) t0 = now;
+            if (now - t0 > (uint64_t)limit_us * 1000u) return false;
+        }
+    }
 }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -28,10 +28,10 @@
 namespace prox {
 namespace {
 
-constexpr int kKT = 64;             // keys of a tile
 constexpr int kWarps = 4;           // computing warps
 constexpr int kThreads = 32 * kWarps + 32;
 constexpr int kMaxStages = 8;
+constexpr int kMaxGrid = 512;        // CTAs of a main kernel
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -68,12 +68,14 @@ struct Cfg {
     static constexpr int KG = kWarps / RG;        // key groups
     static constexpr int WK = kKT / KG;           // keys of a tile one warp takes
     static constexpr int ROWS = 16 * RG;
-    static constexpr TileShape TS{ROWS, kKT};
     static constexpr int NST = D == 128 ? 3 : 6;  // ring stages
     static constexpr int HALF = kKT * 128;        // bytes of 64 elements of a tile's rows
     static constexpr int TILE = HALF * (D / 64);  // bytes of a tile of k (or v)
     static constexpr int OBUF = 16 * D * 4 / 2;   // half of a warp's outputs
 };
+
+// (control data lies behind the line in shared memory)
+static_assert(sizeof(Line) % 16 == 0, "barriers are 8-byte aligned");
 
 struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages];
@@ -126,10 +128,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
     }
     pdl_wait();
     pdl_launch();
-    build_line(ln, a, C::TS, blockIdx.x == 0);  // (its barriers cover the mbarriers too)
-    const long long run = run_length(ln, a.n, a.grid);
-    const long long begin = blockIdx.x * run, end = min(begin + run, ln.pre[a.n]);
-    if (begin >= end) return;
+    build_line(ln, a, ROWS, blockIdx.x == 0);  // (its barriers cover the mbarriers too)
+    const int run = run_length(ln, a.n, a.grid), total = ln.pre[a.n];
+    if (blockIdx.x > (total - 1) / run || total == 0) return;
+    const int begin = blockIdx.x * run, end = begin + min(run, total - begin);
     const int per_box = min(ps, kKT);           // rows of a box
     const int boxes = kKT / per_box;            // pages of a tile
 
@@ -141,8 +143,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
         const int pg = lane / (2 * H), kv = lane / H & 1, half = lane % H;
         bool live = true;
         int it = 0;
-        for (long long pos = begin; pos < end;) {
-            const Stretch st = stretch_at(ln, a, C::TS, pos, end);
+        for (int pos = begin; pos < end;) {
+            const Stretch st = stretch_at(ln, a, ROWS, pos, end);
             pos += st.n_tiles;
             const int tot = ln.tot[st.b];
             const int32_t *table = c.page_table + (size_t)max(ln.seq[st.b], 0) * c.max_pages;
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
             for (int i = 0; i < st.n_tiles; ++i, ++it) {
                 const int tile = st.tile0 + i, slot = it % NST;
                 const int next = i + 1 < st.n_tiles ? page_of(tile + 1) : kNone;
-                if (it >= NST && live && !mbar_wait(&ctl.empty[slot], (it / NST - 1) & 1, a.wait_us)) {
+                if (it >= NST && live && !mbar_spin(&ctl.empty[slot], (it / NST - 1) & 1, a.wait_us)) {
                     live = false;
                     if (lane == 0) atomicOr(c.status, PROX_CACHE_TIMEOUT);
                 }
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
         // after a wait that gave up: let the copies in flight land
         if (!live)
             for (int k = max(0, it - NST); k < it; ++k)
-                mbar_wait(&ctl.full[k % NST], (k / NST) & 1, 1000);
+                mbar_spin(&ctl.full[k % NST], (k / NST) & 1, 1000);
         return;
     }
 
@@ -196,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
     const float sc = a.scale * kLog2e;
     bool live = true;
     int it = 0;
-    for (long long pos = begin; pos < end;) {
-        const Stretch st = stretch_at(ln, a, C::TS, pos, end);
+    for (int pos = begin; pos < end;) {
+        const Stretch st = stretch_at(ln, a, ROWS, pos, end);
         const bool first = pos == begin;
         pos += st.n_tiles;
         const int len = ln.len[st.b], tot = ln.tot[st.b];
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
 
         for (int i = 0; i < st.n_tiles; ++i, ++it) {
             const int tile = st.tile0 + i, slot = it % NST;
-            if (live && !mbar_wait(&ctl.full[slot], (it / NST) & 1, a.wait_us)) {
+            if (live && !mbar_spin(&ctl.full[slot], (it / NST) & 1, a.wait_us)) {
                 live = false;
                 if (lane == 0) atomicOr(c.status, PROX_CACHE_TIMEOUT);
             }
@@ -502,77 +504,122 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
     }
 }
 
-// Joins the pieces of units that were cut, in the order of the line. One CTA
-// takes 32 rows of a unit: lanes are rows, a warp has 1/8 of the columns, so a
-// piece is read in runs of 512 bytes and each warp has several in flight.
+// Joins the pieces of units that were cut. A unit is cut where a CTA's run ends
+// inside it, so the cuts are numbered by the CTAs, and a unit is joined by the
+// first cut in it. The CTAs share out steps of 32 rows and 32 columns: lanes are
+// rows (a piece is read in runs of 512 bytes), the pieces are dealt out to the
+// warps, whose sums meet in shared memory in a fixed order.
 template <int D, int DT>
 __global__ void __launch_bounds__(256)
-    k_attention_join(const __grid_constant__ AttnArgs a, TileShape ts, int max_rows) {
+    k_attention_join(const __grid_constant__ AttnArgs a, int ROWS) {
     __shared__ Line ln;
+    __shared__ float s_o[8][32][32], s_m[8][32], s_l[8][32];
+    __shared__ uint16_t s_cut[kMaxGrid];
+    __shared__ int s_warp[8], s_count;
     // The line depends on the call's inputs alone, which were there before the
     // main kernel let this one start; its pieces come after the wait.
-    build_line(ln, a, ts, false);
+    build_line(ln, a, ROWS, false);
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int groups = (max_rows + 31) / 32, heads = a.cache.n_kv_heads;
-    const int grp = blockIdx.x % groups, bh = blockIdx.x / groups;
-    const int head = bh % heads, b = bh / heads;
-    const int G = a.n_heads / heads, n_rows = ln.rows[b] * G;
-    const int row0 = grp * 32, r = row0 + lane;
-    if (row0 < n_rows) {
-        const int rt = (n_rows + ts.rows - 1) / ts.rows, kt = key_tiles(ln.tot[b], ts);
-        const long long run = run_length(ln, a.n, a.grid);
-        const long long u0 = ln.pre[b] + ((long long)head * rt + row0 / ts.rows) * kt, u1 = u0 + kt;
-        const long long c0 = u0 / run, c1 = (u1 - 1) / run;
-        if (c0 != c1) {  // else written by its CTA
-            pdl_wait();
-            const int rr = r % ts.rows;
-            // (rows behind the last one read their neighbours' place in the piece)
-            auto at = [&](long long c) { return piece(a, c, c * run >= u0, D, ts.rows); };
-            float M = -INFINITY;
-#pragma unroll 8
-            for (long long c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(at(c) + ts.rows * D + rr));
-            const float mu = M == -INFINITY ? 0.f : M;
-            constexpr int V = D / 32;  // float4 columns of a warp
-            float o[V][4] = {}, l = 0.f;
-#pragma unroll 4
-            for (long long c = c0; c <= c1; ++c) {
-                const float *p = at(c);
-                const float f = ex2(__ldcg(p + ts.rows * D + rr) - mu);
-                l += f * __ldcg(p + ts.rows * (D + 1) + rr);
+    const int G = a.n_heads / a.cache.n_kv_heads;
+    const int row_groups = (ROWS + 31) / 32, per_cut = row_groups * (D / 32);
+    const int run = run_length(ln, a.n, a.grid), total = ln.pre[a.n];
+    // the cuts that join a unit: inside one, and the first there
+    const int cuts = total ? (total - 1) / run : 0;
+    if (threadIdx.x == 0) s_count = 0;
+    __syncthreads();
+    for (int b = 0; b < cuts; b += 256) {
+        const int j = b + threadIdx.x, cut = (j + 1) * run;
+        bool joins = false;
+        if (j < cuts) {
+            const Stretch st = stretch_at(ln, a, ROWS, cut, total);
+            joins = st.tile0 > 0 && j * run <= cut - st.tile0;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, joins);
+        if (lane == 0) s_warp[wid] = __popc(who);
+        __syncthreads();
+        int at = s_count;
+        for (int w = 0; w < wid; ++w) at += s_warp[w];
+        if (joins) s_cut[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)j;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int w = 0; w < 8; ++w) s_count += s_warp[w];
+        __syncthreads();
+    }
+    const int items = s_count * per_cut;
+    bool waited = false;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int j = s_cut[item / per_cut], rest = item % per_cut, cut = (j + 1) * run;
+        const Stretch st = stretch_at(ln, a, ROWS, cut, total);
+        const int u0 = cut - st.tile0, u1 = u0 + st.all_tiles;
+        const int cc = rest % (D / 32), row0 = st.row_tile * ROWS + rest / (D / 32) * 32;
+        const int n_rows = ln.rows[st.b] * G;
+        if (row0 >= n_rows) continue;
+        const int r = row0 + lane, rr = r % ROWS;  // (rows behind the last: any row's place)
+        const int c1 = (u1 - 1) / run;
+        if (!waited) pdl_wait();
+        waited = true;
+        // pieces j .. c1, this warp's ones under a running maximum
+        float M = -INFINITY, l = 0.f;
+        float4 o[8] = {};
+#pragma unroll 2
+        for (int c = j + wid; c <= c1; c += 8) {
+            const float *p = piece(a, c, c * run >= u0, D, ROWS);
+            const float4 *x = reinterpret_cast<const float4 *>(p) + cc * 8 * ROWS + rr;
+            float4 v[8];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float4 x =
-                        __ldcg(reinterpret_cast<const float4 *>(p) + (size_t)(wid * V + v) * ts.rows + rr);
-                    o[v][0] = fmaf(f, x.x, o[v][0]);
-                    o[v][1] = fmaf(f, x.y, o[v][1]);
-                    o[v][2] = fmaf(f, x.z, o[v][2]);
-                    o[v][3] = fmaf(f, x.w, o[v][3]);
-                }
+            for (int k = 0; k < 8; ++k) v[k] = __ldcg(x + k * ROWS);
+            const float pm = __ldcg(p + ROWS * D + rr), pl = __ldcg(p + ROWS * (D + 1) + rr);
+            const float nm = fmaxf(M, pm), mu = nm == -INFINITY ? 0.f : nm;
+            const float f0 = ex2(M - mu), f1 = ex2(pm - mu);
+            M = nm;
+            l = l * f0 + pl * f1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                o[k].x = fmaf(f1, v[k].x, o[k].x * f0);
+                o[k].y = fmaf(f1, v[k].y, o[k].y * f0);
+                o[k].z = fmaf(f1, v[k].z, o[k].z * f0);
+                o[k].w = fmaf(f1, v[k].w, o[k].w * f0);
             }
-            if (r < n_rows) {
-                const int t = r / G, hq = head * G + r - t * G;
-                const size_t row = ln.row0[b] + t;
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint32_t w[V * 2];
+        }
+        const int parts = min(c1 - j + 1, 8);
+        __syncthreads();  // the last step's sums are read
+        if (wid < parts) {
+            s_m[wid][lane] = M;
+            s_l[wid][lane] = l;
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    w[2 * v] = pack2<DT>(o[v][0] * inv, o[v][1] * inv);
-                    w[2 * v + 1] = pack2<DT>(o[v][2] * inv, o[v][3] * inv);
-                }
-                uint16_t *op = a.out + row * a.out_stride + (size_t)hq * D + wid * V * 4;
-#pragma unroll
-                for (int v = 0; v < V; v += 2)
-                    *reinterpret_cast<uint4 *>(op + v * 4) =
-                        make_uint4(w[2 * v], w[2 * v + 1], w[2 * v + 2], w[2 * v + 3]);
-                if (a.lse && wid == 0)
-                    a.lse[row * a.n_heads + hq] =
-                        M == -INFINITY && l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+            for (int k = 0; k < 8; ++k) {
+                s_o[wid][4 * k][lane] = o[k].x;
+                s_o[wid][4 * k + 1][lane] = o[k].y;
+                s_o[wid][4 * k + 2][lane] = o[k].z;
+                s_o[wid][4 * k + 3][lane] = o[k].w;
             }
+        }
+        __syncthreads();
+        M = -INFINITY;
+        for (int w = 0; w < parts; ++w) M = fmaxf(M, s_m[w][lane]);
+        const float top = M == -INFINITY ? 0.f : M;
+        float y[4] = {};
+        l = 0.f;
+        for (int w = 0; w < parts; ++w) {
+            const float f = ex2(s_m[w][lane] - top);
+            l += f * s_l[w][lane];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = fmaf(f, s_o[w][wid * 4 + k][lane], y[k]);
+        }
+        if (r < n_rows) {
+            const int t = r / G, hq = st.head * G + r - t * G;
+            const size_t row = ln.row0[st.b] + t;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            *reinterpret_cast<uint2 *>(a.out + row * a.out_stride + (size_t)hq * D + cc * 32 + wid * 4) =
+                make_uint2(pack2<DT>(y[0] * inv, y[1] * inv), pack2<DT>(y[2] * inv, y[3] * inv));
+            if (a.lse && cc == 0 && wid == 0)
+                a.lse[row * a.n_heads + hq] =
+                    M == -INFINITY && l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
         }
     }
     // every CTA waits before it ends: what follows this kernel in the stream
-    // may count on the main kernel being done
-    pdl_wait();
+    // counts on the main kernel being done
+    if (!waited) pdl_wait();
     pdl_launch();
 }
 
@@ -600,29 +647,30 @@ cudaError_t run_main(const AttnArgs &a, cudaStream_t s) {
     return launch(k_attention<D, DT, RG>, a.grid, kThreads, smem, s, a);
 }
 
-// How a call runs: row tiles of 16 to 64 rows on mma.sync, of 128 and 256 rows
-// on the tensor memory's MMA
+// How a call runs: row tiles of 16 or 32 rows on mma.sync, of 128 or 256 rows on
+// the tensor memory's MMA
 struct Plan {
-    TileShape ts;
-    int grid_per_sm;
+    int rows, grid_per_sm;
     bool tc;
 };
 Plan plan_of(int max_rows) {
-    if (max_rows <= 16) return {{16, kKT}, 2, false};
-    if (max_rows <= 32) return {{32, kKT}, 2, false};
-    if (max_rows <= 128) return {{128, 128}, 1, true};
-    return {{256, 128}, 1, true};
+    if (max_rows <= 16) return {16, 2, false};
+    if (max_rows <= 32) return {32, 2, false};
+    if (max_rows <= 128) return {128, 1, true};
+    return {256, 1, true};
 }
 
 template <int D, int DT>
 cudaError_t run_typed(const AttnArgs &a, const Plan &p, int max_rows, cudaStream_t s) {
-    cudaError_t e = p.tc              ? launch_attention_tc(a, p.ts.rows / 128, s)
-                    : p.ts.rows == 16 ? run_main<D, DT, 1>(a, s)
+    cudaError_t e = p.tc              ? launch_attention_tc(a, p.rows / 128, s)
+                    : p.rows == 16 ? run_main<D, DT, 1>(a, s)
                                       : run_main<D, DT, 2>(a, s);
     if (e != cudaSuccess) return e;
-    const int groups = (max_rows + 31) / 32;
-    return launch(k_attention_join<D, DT>, a.n * a.cache.n_kv_heads * groups, 256, 0, s, a, p.ts,
-                  max_rows);
+    // no more CTAs than steps if every unit is cut, or than fit on the GPU at once
+    const long long units = (long long)a.n * a.cache.n_kv_heads * ((max_rows + p.rows - 1) / p.rows);
+    const long long steps = min((long long)a.grid - 1, units) * ((p.rows + 31) / 32) * (D / 32);
+    return launch(k_attention_join<D, DT>, (int)min(steps, 4LL * a.grid / p.grid_per_sm), 256, 0, s, a,
+                  p.rows);
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -644,11 +692,11 @@ EncodeFn encode_fn() {
 }
 
 // boxes of 64 elements and up to one page's rows, 128-byte swizzled
-bool encode_rows(CUtensorMap *map, const prox_cache &c, const uint16_t *base, int keys) {
+bool encode_rows(CUtensorMap *map, const prox_cache &c, const uint16_t *base) {
     const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim,
                                 (cuuint64_t)c.n_pages * c.n_kv_heads * c.page_size};
     const cuuint64_t strides[1] = {(cuuint64_t)c.head_dim * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)(c.page_size < keys ? c.page_size : keys)};
+    const cuuint32_t box[2] = {64, (cuuint32_t)(c.page_size < kKT ? c.page_size : kKT)};
     const cuuint32_t ones[2] = {1, 1};
     EncodeFn fn = encode_fn();
     return fn && fn(map,
@@ -662,22 +710,34 @@ bool encode_rows(CUtensorMap *map, const prox_cache &c, const uint16_t *base, in
 
 }  // namespace
 
+// tiles that one sequence can have at most
+static long long tiles_of_one(const prox_cache &c, int max_rows) {
+    const Plan p = plan_of(max_rows);
+    return (long long)c.n_kv_heads * ((max_rows + p.rows - 1) / p.rows) *
+           ((long long)c.max_pages * c.page_size / kKT + 1);
+}
+
+bool attention_fits(const prox_cache &c, int max_rows) { return tiles_of_one(c, max_rows) < 1ll << 31; }
+
 size_t attention_part_bytes(int head_dim, int max_rows, int sms) {
     const Plan p = plan_of(max_rows);
-    return (size_t)sms * p.grid_per_sm * 2 * piece_floats(head_dim, p.ts.rows) * sizeof(float);
+    return (size_t)sms * p.grid_per_sm * 2 * piece_floats(head_dim, p.rows) * sizeof(float);
 }
 
 cudaError_t launch_attention(AttnArgs &a, const uint16_t *k_layer, int max_rows, int sms,
                              cudaStream_t s) {
     const Plan p = plan_of(max_rows);
-    if (!encode_rows(&a.map_k, a.cache, k_layer, p.ts.keys) ||
-        !encode_rows(&a.map_v, a.cache, a.v_layer, p.ts.keys))
+    if (!encode_rows(&a.map_k, a.cache, k_layer) ||
+        !encode_rows(&a.map_v, a.cache, a.v_layer))
         return cudaErrorInvalidValue;
-    a.grid = sms * p.grid_per_sm;
+    a.grid = min(sms * p.grid_per_sm, kMaxGrid);
     const int32_t *seqs = a.seqs, *cu = a.cu_q;
     const int n = a.n;
-    for (int at = 0; at < n; at += kGroup) {
-        a.n = n - at < kGroup ? n - at : kGroup;
+    // sequences of a launch: at most kGroup, and fewer than 2^31 tiles
+    const long long most = tiles_of_one(a.cache, max_rows);
+    const int group = (int)min((long long)kGroup, 0x7fffffffLL / most);
+    for (int at = 0; at < n; at += group) {
+        a.n = n - at < group ? n - at : group;
         a.seqs = seqs + at;
         a.cu_q = cu + at;
         cudaError_t e;

@@ -1,14 +1,14 @@
 // Tree attention for more than a few rows of a key/value head: both products
 // on the tensor memory's MMA (tcgen05), 128 rows a row group, one or two row
-// groups a CTA, 128 keys a tile. The arithmetic and the line of tiles are those
-// of k_attention.cu; what differs is where things live:
+// groups a CTA. The arithmetic and the line of tiles are those of
+// k_attention.cu; what differs is where things live:
 //
 //   q        shared memory, K-major, 128-byte swizzle (written by the row
 //            group's threads: rows are (token, head) pairs of a strided tensor)
-//   k, v     a ring of shared-memory slots of 128 rows, filled by tensor-map
+//   k, v     a ring of shared-memory slots of 64 rows, filled by tensor-map
 //            boxes; v is the second product's N-major operand as it lies
-//   scores   tensor memory, one lane a row: a thread owns its row, so maxima
-//            and sums need no exchange
+//   scores   tensor memory, two buffers of 64 columns a row group, one lane a
+//            row: a thread owns its row, so maxima and sums need no exchange
 //   probabilities over the scores they came from, in 16 bits, as the second
 //            product's tensor-memory operand
 //   outputs  tensor memory, fp32. They are rescaled only when a row's maximum
@@ -16,8 +16,8 @@
 //            e^(x - offset) <= 2^8 loses nothing in fp32 sums.
 //
 // One warp loads, one thread issues the MMAs, and four warps a row group do the
-// softmax. With two row groups one computes probabilities while the other's
-// products run, and k and v are read once for 256 rows.
+// softmax. The next tile's scores are formed while this one's probabilities
+// are, so the softmax warps always have work; k and v are read once for 256 rows.
 #include "attention.cuh"
 #include "umma.cuh"
 
@@ -26,26 +26,32 @@
 namespace prox {
 namespace {
 
-constexpr int kKT = 128;            // keys of a tile
-constexpr int kMaxSlots = 10;
+constexpr int kMaxSlots = 20;
 constexpr float kGrow = 8.f;        // log2 units a maximum may grow before outputs are rescaled
 
 template <int D, int NWG>
 struct Cfg {
     static constexpr int ROWS = 128 * NWG;
-    static constexpr TileShape TS{ROWS, kKT};
     static constexpr int H = D / 64;              // 128-byte columns of a row
-    static constexpr int HALF = kKT * 128;        // bytes of one of them
-    static constexpr int TILE = HALF * H;         // bytes of a tile of k (or v), or of a group's q
-    // slots of the ring: what fits beside q in 200 KB
-    static constexpr int SLOTS = D == 128 ? (NWG == 2 ? 4 : 5) : (NWG == 2 ? 8 : 10);
+    static constexpr int HALF = kKT * 128;        // bytes of one of them, of a tile of k (or v)
+    static constexpr int TILE = HALF * H;         // bytes of a tile of k (or v)
+    static constexpr int QHALF = 128 * 128, QTILE = QHALF * H;  // the same of a group's q
+    // slots of the ring: what fits beside q in 210 KB
+    static constexpr int SLOTS = (210 * 1024 - NWG * QTILE) / TILE < kMaxSlots
+                                     ? (210 * 1024 - NWG * QTILE) / TILE
+                                     : kMaxSlots;
     static constexpr int THREADS = 128 * NWG + 64;
     static constexpr uint32_t COLS = NWG == 2 ? 512 : 256;  // tensor-memory columns
 };
 
+// (control data lies behind the line in shared memory)
+static_assert(sizeof(Line) % 16 == 0, "barriers are 8-byte aligned");
+
 struct Ctl {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
-    uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2];
+    // per row group: q written; scores there and probabilities there (two
+    // buffers); a tile's second product done
+    uint64_t q_ready[2], s_full[2][2], p_ready[2][2], o_done[2];
     uint64_t poison[4];             // drafted tokens whose v has an infinity or NaN
     uint32_t tmem;
 };
@@ -53,7 +59,7 @@ struct Ctl {
 template <int D, int NWG>
 constexpr size_t smem_bytes() {
     using C = Cfg<D, NWG>;
-    return 1024 + (size_t)(NWG + C::SLOTS) * C::TILE + sizeof(Line) + sizeof(Ctl);
+    return 1024 + (size_t)NWG * C::QTILE + (size_t)C::SLOTS * C::TILE + sizeof(Line) + sizeof(Ctl);
 }
 
 // D (fp32) (+)= A (16-bit, tensor memory) x B^T
@@ -104,10 +110,58 @@ __device__ __forceinline__ void tmem_get32(uint32_t taddr, uint32_t (&v)[32]) {
         : "memory");
 }
 
+// 32 columns of this thread's lane on their way; tmem_take32 makes them usable
+__device__ __forceinline__ void tmem_ask32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
+          "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+// (the registers go through the wait, so that no use of them can precede it)
+__device__ __forceinline__ void tmem_take32(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                   "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                   "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                   "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                   "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+
+// two fp32 operations an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // bounded wait; once one has given up, later ones do not wait at all
 __device__ __forceinline__ void wait_or_give_up(uint64_t *bar, uint32_t count, const AttnArgs &a,
                                                 bool &live) {
-    if (live && !mbar_wait(bar, count & 1, a.wait_us)) {
+    if (live && !mbar_spin(bar, count & 1, a.wait_us)) {
         live = false;
         atomicOr(a.cache.status, PROX_CACHE_TIMEOUT);
     }
@@ -121,7 +175,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
     extern __shared__ unsigned char raw[];
     unsigned char *sq = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    unsigned char *ring = sq + NWG * C::TILE;
+    unsigned char *ring = sq + NWG * C::QTILE;
     Line &ln = *reinterpret_cast<Line *>(ring + SLOTS * C::TILE);
     Ctl &ctl = *reinterpret_cast<Ctl *>(&ln + 1);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -135,35 +189,41 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
         }
         for (int w = 0; w < NWG; ++w) {
             mbar_init(&ctl.q_ready[w], 4);
-            mbar_init(&ctl.s_full[w], 1);
-            mbar_init(&ctl.p_ready[w], 4);
-            mbar_init(&ctl.o_full[w], 1);
+            mbar_init(&ctl.o_done[w], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&ctl.s_full[w][b], 1);
+                mbar_init(&ctl.p_ready[w][b], 4);
+            }
         }
         mbar_fence_init();
     }
     if (wid == 4 * NWG) tmem_alloc(&ctl.tmem, C::COLS);
+    if (wid == 4 * NWG + 1 && lane < 2)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(
+                         reinterpret_cast<uint64_t>(lane ? &a.map_v : &a.map_k))
+                     : "memory");
     pdl_wait();
     pdl_launch();
     tc_fence_before();
-    build_line(ln, a, C::TS, blockIdx.x == 0);  // (its barriers cover the setup above)
+    build_line(ln, a, ROWS, blockIdx.x == 0);  // (its barriers cover the setup above)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
     const uint32_t t_s = tmem, t_o = tmem + NWG * 128;  // + 128 per row group
-    const long long run = run_length(ln, a.n, a.grid);
-    const long long begin = min(blockIdx.x * run, ln.pre[a.n]);
-    const long long end = min(begin + run, ln.pre[a.n]);
+    const int run = run_length(ln, a.n, a.grid), total = ln.pre[a.n];
+    const bool idle = total == 0 || blockIdx.x > (total - 1) / run;
+    const int begin = idle ? 0 : blockIdx.x * run, end = idle ? 0 : begin + min(run, total - begin);
     const int per_box = min(ps, kKT), boxes = kKT / per_box;
     bool live = true;
 
     if (wid == 4 * NWG + 1) {
         // ------------------------------------------------------------------
-        // loading warp: lane = (page of the tile, 64 elements); slot sequence
-        // k0, v0, k1, v1, ...
+        // loading warp: lane = (page of the tile, 64 elements); the order of
+        // slots is that of use: k0, k1, v0, k2, v1, ..., v last
         // ------------------------------------------------------------------
         const int pg = lane / H, half = lane % H;
         int it = 0;
-        for (long long pos = begin; pos < end;) {
-            const Stretch st = stretch_at(ln, a, C::TS, pos, end);
+        for (int pos = begin; pos < end && live;) {
+            const Stretch st = stretch_at(ln, a, ROWS, pos, end);
             pos += st.n_tiles;
             const int tot = ln.tot[st.b];
             const int32_t *table = c.page_table + (size_t)max(ln.seq[st.b], 0) * c.max_pages;
@@ -171,99 +231,110 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                 const int key = tile * kKT + pg * per_box;
                 return pg < boxes && key < tot ? table[key / ps] : kNone;
             };
-            int page = page_of(st.tile0);
-            for (int i = 0; i < st.n_tiles; ++i) {
-                const int tile = st.tile0 + i;
-                const int next = i + 1 < st.n_tiles ? page_of(tile + 1) : kNone;
+            // one tile of k or v into the next slot
+            auto load = [&](const CUtensorMap *map, int tile, int page) {
+                const int slot = it % SLOTS;
+                if (it >= SLOTS && !mbar_spin(&ctl.empty[slot], (it / SLOTS - 1) & 1, a.wait_us)) {
+                    live = false;
+                    if (lane == 0) atomicOr(c.status, PROX_CACHE_TIMEOUT);
+                    return;
+                }
                 // a page id out of range: zeros (a box outside the map), and the mask
-                const bool wanted = page != kNone, good = page >= 0 && page < c.n_pages;
-                const unsigned bad = __ballot_sync(0xffffffffu, wanted && !good);
+                const bool wanted = page != kNone, good = page_ok(c, page);
                 const unsigned load = __ballot_sync(0xffffffffu, wanted);
-                if (bad && lane == 0) atomicOr(c.status, PROX_CACHE_BAD_STATE);
                 const int y = good ? (page * c.n_kv_heads + st.head) * ps + tile * kKT % ps
                                    : c.n_pages * c.n_kv_heads * ps;
-                for (int kv = 0; kv < 2; ++kv, ++it) {
-                    const int slot = it % SLOTS;
-                    if (it >= SLOTS) {
-                        const bool was = live;
-                        if (live && !mbar_wait(&ctl.empty[slot], (it / SLOTS - 1) & 1, a.wait_us))
-                            live = false;
-                        if (was && !live && lane == 0) atomicOr(c.status, PROX_CACHE_TIMEOUT);
-                    }
-                    if (!live) break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&ctl.full[slot], __popc(load) * per_box * 128);
-                    __syncwarp();
-                    if (wanted)
-                        asm volatile(
-                            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::"
-                            "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                                smem_addr(ring) + slot * C::TILE + half * C::HALF + pg * per_box * 128),
-                            "l"(reinterpret_cast<uint64_t>(kv ? &a.map_v : &a.map_k)),
-                            "r"(half * 64), "r"(y), "r"(smem_addr(&ctl.full[slot]))
-                            : "memory");
+                if (wanted && !good) atomicOr(c.status, PROX_CACHE_BAD_STATE);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&ctl.full[slot], __popc(load) * per_box * 128);
+                __syncwarp();
+                if (wanted)
+                    box_g2s(smem_addr(ring) + slot * C::TILE + half * C::HALF + pg * per_box * 128,
+                            map, half * 64, y, &ctl.full[slot]);
+                ++it;
+            };
+            int now = page_of(st.tile0), next = kNone;
+            load(&a.map_k, st.tile0, now);
+            for (int i = 0; i < st.n_tiles && live; ++i) {
+                const int tile = st.tile0 + i;
+                if (i + 1 < st.n_tiles) {
+                    next = page_of(tile + 1);
+                    load(&a.map_k, tile + 1, next);
                 }
-                if (!live) break;
-                page = next;
+                if (live) load(&a.map_v, tile, now);
+                now = next;
             }
-            if (!live) break;
         }
         // after a wait that gave up: let the copies in flight land
         if (!live)
             for (int k = max(0, it - SLOTS); k < it; ++k)
-                mbar_wait(&ctl.full[k % SLOTS], (k / SLOTS) & 1, 1000);
+                mbar_spin(&ctl.full[k % SLOTS], (k / SLOTS) & 1, 1000);
     } else if (wid == 4 * NWG) {
         // ------------------------------------------------------------------
         // the thread that issues the MMAs
         // ------------------------------------------------------------------
         if (lane == 0) {
             constexpr uint32_t qk_idesc = idesc_of<DT>(kKT, false), pv_idesc = idesc_of<DT>(D, true);
-            const uint32_t qa = smem_addr(sq), ra = smem_addr(ring);
-            int it = 0;
-            uint32_t n_q[2] = {}, n_p[2] = {};
+            // descriptors of the first q, k and v tiles; the address field (in 16
+            // bytes) is the low one and never carries
+            const uint64_t dq = sw128_desc(smem_addr(sq), 16, 1024),
+                           dk = sw128_desc(smem_addr(ring), 16, 1024),
+                           dv = sw128_desc(smem_addr(ring), C::HALF, 1024);
+            uint32_t n_q[2] = {}, n_s[2] = {}, n_p[2] = {};  // scores formed, probabilities used
+            // scores of the tile in slot, into the row group's next buffer
             auto qk = [&](int w, int slot) {
+                const uint64_t q0 = dq + (uint32_t)(w * (C::QTILE >> 4));
+                const uint64_t k0 = dk + (uint32_t)(slot * (C::TILE >> 4));
+                const uint32_t d = t_s + w * 128 + (n_s[w] & 1) * 64;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma(t_s + w * 128,
-                         sw128_desc(qa + w * C::TILE + (k / 4) * C::HALF + (k % 4) * 32, 16, 1024),
-                         sw128_desc(ra + slot * C::TILE + (k / 4) * C::HALF + (k % 4) * 32, 16, 1024),
-                         qk_idesc, k > 0);
-                umma_commit(&ctl.s_full[w]);
+                    umma(d, q0 + (k / 4) * (C::QHALF >> 4) + (k % 4) * 2,
+                         k0 + (k / 4) * (C::HALF >> 4) + (k % 4) * 2, qk_idesc, k > 0);
+                umma_commit(&ctl.s_full[w][n_s[w]++ & 1]);
             };
-            for (long long pos = begin; pos < end;) {
-                const Stretch st = stretch_at(ln, a, C::TS, pos, end);
+            int slot = 0, turn = 0;  // of the next slot in the order of loading
+            auto await = [&] { wait_or_give_up(&ctl.full[slot], turn, a, live); };
+            auto next = [&] {
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    ++turn;
+                }
+            };
+            for (int pos = begin; pos < end;) {
+                const Stretch st = stretch_at(ln, a, ROWS, pos, end);
                 pos += st.n_tiles;
                 const int groups =
                     NWG == 2 && ln.rows[st.b] * G - st.row_tile * ROWS > 128 ? 2 : 1;
-                wait_or_give_up(&ctl.full[it % SLOTS], it / SLOTS, a, live);
+                // k of tile 0, then k of tile i + 1 and v of tile i
+                await();
                 for (int w = 0; w < groups; ++w) {
                     wait_or_give_up(&ctl.q_ready[w], n_q[w]++, a, live);
                     tc_fence_after();
-                    qk(w, it % SLOTS);
+                    qk(w, slot);
                 }
-                umma_commit(&ctl.empty[it % SLOTS]);
+                umma_commit(&ctl.empty[slot]);
+                next();
                 for (int i = 0; i < st.n_tiles; ++i) {
-                    const int sv = (it + 1) % SLOTS, sk = (it + 2) % SLOTS;
-                    const bool more = i + 1 < st.n_tiles;
-                    wait_or_give_up(&ctl.full[sv], (it + 1) / SLOTS, a, live);
+                    if (i + 1 < st.n_tiles) {
+                        await();
+                        for (int w = 0; w < groups; ++w) qk(w, slot);
+                        umma_commit(&ctl.empty[slot]);
+                        next();
+                    }
+                    await();
+                    const uint64_t v0 = dv + (uint32_t)(slot * (C::TILE >> 4));
                     for (int w = 0; w < groups; ++w) {
-                        wait_or_give_up(&ctl.p_ready[w], n_p[w]++, a, live);
+                        const uint32_t buf = n_p[w] & 1;
+                        wait_or_give_up(&ctl.p_ready[w][buf], n_p[w]++ >> 1, a, live);
                         tc_fence_after();
 #pragma unroll
                         for (int k = 0; k < kKT / 16; ++k)
-                            umma_ts(t_o + w * 128, t_s + w * 128 + k * 8,
-                                    sw128_desc(ra + sv * C::TILE + k * 2048, C::HALF, 1024),
-                                    pv_idesc, i > 0 || k > 0);
-                        if (w == groups - 1) umma_commit(&ctl.empty[sv]);
-                        if (more) {
-                            if (w == 0) wait_or_give_up(&ctl.full[sk], (it + 2) / SLOTS, a, live);
-                            qk(w, sk);
-                            if (w == groups - 1) umma_commit(&ctl.empty[sk]);
-                        } else {
-                            umma_commit(&ctl.o_full[w]);
-                        }
+                            umma_ts(t_o + w * 128, t_s + w * 128 + buf * 64 + k * 8,
+                                    v0 + k * (2048 >> 4), pv_idesc, i > 0 || k > 0);
+                        umma_commit(&ctl.o_done[w]);
                     }
-                    it += 2;
+                    umma_commit(&ctl.empty[slot]);
+                    next();
                 }
             }
         }
@@ -274,12 +345,12 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
         // ------------------------------------------------------------------
         const int w = wid >> 2, t = tid & 127;
         const uint32_t lane_at = (uint32_t)(wid & 3) << 21;   // first tensor-memory lane << 16
-        const uint32_t ts = t_s + w * 128 + lane_at, to = t_o + w * 128 + lane_at;
+        const uint32_t to = t_o + w * 128 + lane_at;
         const float sc = a.scale * kLog2e;
-        int it = 0;
-        uint32_t n_s = 0, n_o = 0;
-        for (long long pos = begin; pos < end;) {
-            const Stretch st = stretch_at(ln, a, C::TS, pos, end);
+        uint32_t n_s = 0, n_o = 0;  // tiles of this row group so far
+        int it = 0;                 // slots used by the stretches so far
+        for (int pos = begin; pos < end;) {
+            const Stretch st = stretch_at(ln, a, ROWS, pos, end);
             const bool first = pos == begin;
             pos += st.n_tiles;
             const int len = ln.len[st.b], tot = ln.tot[st.b];
@@ -299,12 +370,12 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
             {
                 // q: 16-byte pieces; rows behind the last one are zeros
                 const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * a.q_stride + (size_t)head * D);
-                unsigned char *dst = sq + w * C::TILE + t * 128;
+                unsigned char *dst = sq + w * C::QTILE + t * 128;
                 if (busy) {
 #pragma unroll
                     for (int x = 0; x < D / 8; ++x) {
                         const uint4 v = there ? src[x] : make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(dst + (x >> 3) * C::HALF +
+                        *reinterpret_cast<uint4 *>(dst + (x >> 3) * C::QHALF +
                                                    (((x & 7) ^ (t & 7)) << 4)) = v;
                     }
                 }
@@ -322,11 +393,12 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
             };
             int page = peek(st.tile0);
             float m = -INFINITY, l = 0.f;   // offset in use (log2 units) and sum
-            for (int i = 0; i < st.n_tiles; ++i, it += 2) {
+            for (int i = 0; i < st.n_tiles; ++i) {
                 const int tile = st.tile0 + i;
                 const uint32_t bad = __ballot_sync(0xffffffffu, !page_ok(c, page));
                 page = i + 1 < st.n_tiles ? peek(tile + 1) : 0;
-                wait_or_give_up(&ctl.s_full[w], n_s++, a, live);
+                const uint32_t buf = n_s & 1, ts = t_s + w * 128 + buf * 64 + lane_at;
+                wait_or_give_up(&ctl.s_full[w][buf], n_s++ >> 1, a, live);
                 tc_fence_after();
                 const bool edge = (tile + 1) * kKT > len;
                 if (w == 0 && edge) {
@@ -334,10 +406,12 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                     // key: rows behind the last key (0 * inf is not 0), and the
                     // infinities and NaN of drafted tokens, which only some rows
                     // see; those come back when the outputs are written
-                    const int sv = (it + 1) % SLOTS, key = tile * kKT + t;
-                    wait_or_give_up(&ctl.full[sv], (it + 1) / SLOTS, a, live);
-                    unsigned char *vr = ring + sv * C::TILE + t * 128;
-                    if (key >= tot) {
+                    const int key = tile * kKT + t;
+                    const int at = it + (i + 1 < st.n_tiles ? 2 * i + 2 : 2 * i + 1), slot = at % SLOTS;
+                    wait_or_give_up(&ctl.full[slot], at / SLOTS, a, live);
+                    unsigned char *vr = ring + slot * C::TILE + t * 128;
+                    if (t >= kKT) {
+                    } else if (key >= tot) {
 #pragma unroll
                         for (int x = 0; x < D / 8; ++x)
                             *reinterpret_cast<uint4 *>(vr + (x >> 3) * C::HALF + (x & 7) * 16) =
@@ -366,44 +440,37 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                 }
                 if (busy) {
                     const bool masked = edge || bad;
-                    uint64_t seen[2] = {~0ull, ~0ull};
+                    uint64_t seen = ~0ull;
+                    if (masked) {
+                        uint64_t ok = low_bits(tot - tile * kKT);
+                        for (int p = 0; p < boxes; ++p)
+                            if (bad >> p & 1) ok &= ~(low_bits(per_box) << (p * per_box));
+                        seen = there ? seen_bits(tree, a.tree_words, len, tok, tile * kKT) & ok : 0ull;
+                    }
+                    uint32_t s[kKT], p[kKT / 2];
+                    tmem_ask32(ts, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                    tmem_ask32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                    tmem_take32(*reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                    tmem_take32(*reinterpret_cast<uint32_t(*)[32]>(&s[32]));
                     if (masked) {
 #pragma unroll
-                        for (int hw = 0; hw < 2; ++hw) {
-                            const int w0 = tile * kKT + hw * 64;
-                            uint64_t ok = low_bits(tot - w0);
-                            for (int p = 0; p < boxes; ++p)
-                                if (bad >> p & 1) {
-                                    const int lo = p * per_box - hw * 64;
-                                    ok &= ~(low_bits(lo + per_box) & ~low_bits(lo));
-                                }
-                            seen[hw] = there ? seen_bits(tree, a.tree_words, len, tok, w0) & ok : 0ull;
-                        }
+                        for (int x = 0; x < kKT; ++x)
+                            if (!(seen >> x & 1)) s[x] = 0xff800000u;
                     }
-                    // the row's maximum, then its probabilities over the scores
-                    float mx = -INFINITY;
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int q = 0; q < kKT / 32; ++q) {
-                        uint32_t s[32];
-                        tmem_get32(ts + q * 32, s);
-                        const uint32_t bits = (uint32_t)(seen[q >> 1] >> (q & 1) * 32);
-                        if (masked) {
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (bits >> x & 1) mx = fmaxf(mx, __uint_as_float(s[x]));
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, __uint_as_float(s[x]));
-                        }
-                    }
-                    mx *= sc;
-                    const bool grew = mx > m + kGrow || (mx > m && m == -INFINITY);
-                    if (__any_sync(0xffffffffu, grew)) {
-                        const float nm = fmaxf(m, mx);
+                    for (int x = 0; x < kKT; ++x)
+                        mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                    if (__any_sync(0xffffffffu, top > m + kGrow || (top > m && m == -INFINITY))) {
+                        const float nm = fmaxf(m, top);
                         const float f = nm > m ? ex2(m - nm) : 1.f;
                         m = nm;
                         l *= f;
                         if (i > 0) {
+                            // (products up to the last tile's are in the outputs)
+                            wait_or_give_up(&ctl.o_done[w], n_o - 1, a, live);
+                            tc_fence_after();
 #pragma unroll 1
                             for (int q = 0; q < D / 32; ++q) {
                                 uint32_t o[32];
@@ -417,35 +484,33 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                         }
                     }
                     const float mu = m == -INFINITY ? 0.f : m;
+                    const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int q = 0; q < kKT / 32; ++q) {
-                        uint32_t s[32], p[16];
-                        tmem_get32(ts + q * 32, s);
-                        if (masked) {
-                            const uint32_t bits = (uint32_t)(seen[q >> 1] >> (q & 1) * 32);
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (!(bits >> x & 1)) s[x] = 0xff800000u;
-                        }
-#pragma unroll
-                        for (int x = 0; x < 32; x += 2) {
-                            const float e0 = ex2(fmaf(__uint_as_float(s[x]), sc, -mu));
-                            const float e1 = ex2(fmaf(__uint_as_float(s[x + 1]), sc, -mu));
-                            l += e0 + e1;
-                            p[x / 2] = pack2<DT>(e0, e1);
-                        }
-                        tmem_st16(ts + q * 16, p);
+                    for (int x = 0; x < kKT; x += 2) {
+                        const float2 z = fma2(
+                            make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), sc2, mu2);
+                        const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                        sum[x / 2 & 1] = add2(sum[x / 2 & 1], e);
+                        p[x / 2] = pack2<DT>(e.x, e.y);
                     }
+                    sum[0] = add2(sum[0], sum[1]);
+                    l += sum[0].x + sum[0].y;
+#pragma unroll
+                    for (int q = 0; q < kKT / 32; ++q)
+                        tmem_st16(ts + q * 16, *reinterpret_cast<uint32_t(*)[16]>(&p[q * 16]));
                     tmem_st_wait();
                 }
+                ++n_o;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_ready[w]);
+                if (lane == 0) mbar_arrive(&ctl.p_ready[w][buf]);
             }
+            it += 2 * st.n_tiles;
             // --------------------------------------------------------------
             // the rows' outputs, or a piece of them
             // --------------------------------------------------------------
-            wait_or_give_up(&ctl.o_full[w], n_o++, a, live);
+            wait_or_give_up(&ctl.o_done[w], n_o - 1, a, live);
             tc_fence_after();
             if (busy) {
                 const bool whole = st.n_tiles == st.all_tiles;

@@ -183,7 +183,8 @@ prox_status prox_cache_status(const prox_cache *cache, void *stream, uint32_t *f
  * Arithmetic: scores, softmax statistics and sums in fp32; the probabilities
  * are rounded to the cache's type for the product with v.
  * A sequence may be listed several times. n <= 65536, n_heads a multiple of
- * n_kv_heads, n_heads <= 64 * n_kv_heads.
+ * n_kv_heads, n_heads <= 64 * n_kv_heads; n_kv_heads * (max_pages * page_size
+ * / 64 + 1) < 2^31 / 64.
  */
 size_t prox_attention_workspace_bytes(const prox_cache *cache, int n_heads, int max_q);
 prox_status prox_tree_attention(const prox_cache *cache, int layer, int n, const int32_t *seqs,
