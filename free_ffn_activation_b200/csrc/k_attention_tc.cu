@@ -158,6 +158,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// one thread of the warp, the same one each time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// a value that is the same in all lanes, in a form that says so
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+    return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // bounded wait; once one has given up, later ones do not wait at all
 __device__ __forceinline__ void wait_or_give_up(uint64_t *bar, uint32_t count, const AttnArgs &a,
                                                 bool &live) {
@@ -271,71 +287,86 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                 mbar_spin(&ctl.full[k % SLOTS], (k / SLOTS) & 1, 1000);
     } else if (wid == 4 * NWG) {
         // ------------------------------------------------------------------
-        // the thread that issues the MMAs
+        // the warp that issues the MMAs: one elected thread does, but the whole
+        // warp runs the loops on values it knows to be uniform, so that operand
+        // descriptors live in uniform registers (computed by one thread alone,
+        // an MMA took 90 cycles to issue, twice what it takes to run)
         // ------------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t qk_idesc = idesc_of<DT>(kKT, false), pv_idesc = idesc_of<DT>(D, true);
-            // descriptors of the first q, k and v tiles; the address field (in 16
-            // bytes) is the low one and never carries
-            const uint64_t dq = sw128_desc(smem_addr(sq), 16, 1024),
-                           dk = sw128_desc(smem_addr(ring), 16, 1024),
-                           dv = sw128_desc(smem_addr(ring), C::HALF, 1024);
-            uint32_t n_q[2] = {}, n_s[2] = {}, n_p[2] = {};  // scores formed, probabilities used
-            // scores of the tile in slot, into the row group's next buffer
-            auto qk = [&](int w, int slot) {
-                const uint64_t q0 = dq + (uint32_t)(w * (C::QTILE >> 4));
-                const uint64_t k0 = dk + (uint32_t)(slot * (C::TILE >> 4));
-                const uint32_t d = t_s + w * 128 + (n_s[w] & 1) * 64;
+        constexpr uint32_t qk_idesc = idesc_of<DT>(kKT, false), pv_idesc = idesc_of<DT>(D, true);
+        // low words of the descriptors of the first q, k and v tiles (the address
+        // field, in 16 bytes, never carries); the high words are constants
+        const uint32_t q_lo = uniform((uint32_t)sw128_desc(smem_addr(sq), 16, 1024)),
+                       k_lo = uniform((uint32_t)sw128_desc(smem_addr(ring), 16, 1024)),
+                       v_lo = uniform((uint32_t)sw128_desc(smem_addr(ring), C::HALF, 1024));
+        constexpr uint64_t hi = (uint64_t)(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
+        const uint32_t d_s = uniform(t_s), d_o = uniform(t_o);
+        const bool one = elect_one();
+        uint32_t n_q[2] = {}, n_s[2] = {}, n_p[2] = {};  // scores formed, probabilities used
+        int slot = 0, turn = 0;                       // of the next slot in the order of loading
+        auto await = [&] { wait_or_give_up(&ctl.full[slot], turn, a, live); };
+        auto next = [&] {
+            if (++slot == SLOTS) {
+                slot = 0;
+                ++turn;
+            }
+        };
+        // scores of the slot's tile, into the row group's next buffer
+        auto qk = [&](int w) {
+            const uint32_t d = d_s + w * 128 + (n_s[w] & 1) * 64;
+            const uint32_t k0 = k_lo + slot * (C::TILE >> 4);
+            if (one) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma(d, q0 + (k / 4) * (C::QHALF >> 4) + (k % 4) * 2,
-                         k0 + (k / 4) * (C::HALF >> 4) + (k % 4) * 2, qk_idesc, k > 0);
-                umma_commit(&ctl.s_full[w][n_s[w]++ & 1]);
-            };
-            int slot = 0, turn = 0;  // of the next slot in the order of loading
-            auto await = [&] { wait_or_give_up(&ctl.full[slot], turn, a, live); };
-            auto next = [&] {
-                if (++slot == SLOTS) {
-                    slot = 0;
-                    ++turn;
-                }
-            };
-            for (int pos = begin; pos < end;) {
-                const Stretch st = stretch_at(ln, a, ROWS, pos, end);
-                pos += st.n_tiles;
-                const int groups =
-                    NWG == 2 && ln.rows[st.b] * G - st.row_tile * ROWS > 128 ? 2 : 1;
-                // k of tile 0, then k of tile i + 1 and v of tile i
-                await();
-                for (int w = 0; w < groups; ++w) {
-                    wait_or_give_up(&ctl.q_ready[w], n_q[w]++, a, live);
-                    tc_fence_after();
-                    qk(w, slot);
-                }
-                umma_commit(&ctl.empty[slot]);
-                next();
-                for (int i = 0; i < st.n_tiles; ++i) {
-                    if (i + 1 < st.n_tiles) {
-                        await();
-                        for (int w = 0; w < groups; ++w) qk(w, slot);
-                        umma_commit(&ctl.empty[slot]);
-                        next();
-                    }
+                    umma(d, hi | (q_lo + w * (C::QTILE >> 4) + (k / 4) * (C::QHALF >> 4) + (k % 4) * 2),
+                         hi | (k0 + (k / 4) * (C::HALF >> 4) + (k % 4) * 2), qk_idesc, k > 0);
+                umma_commit(&ctl.s_full[w][n_s[w] & 1]);
+            }
+            ++n_s[w];
+        };
+        for (int pos = begin; pos < end;) {
+            const Stretch st = stretch_at(ln, a, ROWS, pos, end);
+            pos += st.n_tiles;
+            const int n_tiles = uniform(st.n_tiles);
+            const bool two = NWG == 2 && uniform(ln.rows[st.b] * G - st.row_tile * ROWS > 128 ? 1 : 0);
+            // k of tile 0, then k of tile i + 1 and v of tile i
+            await();
+            wait_or_give_up(&ctl.q_ready[0], n_q[0]++, a, live);
+            tc_fence_after();
+            qk(0);
+            if (two) {
+                wait_or_give_up(&ctl.q_ready[1], n_q[1]++, a, live);
+                tc_fence_after();
+                qk(1);
+            }
+            if (one) umma_commit(&ctl.empty[slot]);
+            next();
+            for (int i = 0; i < n_tiles; ++i) {
+                if (i + 1 < n_tiles) {
                     await();
-                    const uint64_t v0 = dv + (uint32_t)(slot * (C::TILE >> 4));
-                    for (int w = 0; w < groups; ++w) {
-                        const uint32_t buf = n_p[w] & 1;
-                        wait_or_give_up(&ctl.p_ready[w][buf], n_p[w]++ >> 1, a, live);
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < kKT / 16; ++k)
-                            umma_ts(t_o + w * 128, t_s + w * 128 + buf * 64 + k * 8,
-                                    v0 + k * (2048 >> 4), pv_idesc, i > 0 || k > 0);
-                        umma_commit(&ctl.o_done[w]);
-                    }
-                    umma_commit(&ctl.empty[slot]);
+                    qk(0);
+                    if (two) qk(1);
+                    if (one) umma_commit(&ctl.empty[slot]);
                     next();
                 }
+                await();
+#pragma unroll
+                for (int w = 0; w < NWG; ++w) {
+                    if (w == 1 && !two) continue;
+                    const uint32_t buf = n_p[w] & 1;
+                    wait_or_give_up(&ctl.p_ready[w][buf], n_p[w] >> 1, a, live);
+                    ++n_p[w];
+                    tc_fence_after();
+                    if (one) {
+#pragma unroll
+                        for (int k = 0; k < kKT / 16; ++k)
+                            umma_ts(d_o + w * 128, d_s + w * 128 + buf * 64 + k * 8,
+                                    hi | (v_lo + slot * (C::TILE >> 4) + k * (2048 >> 4)), pv_idesc,
+                                    k > 0 || i > 0);
+                        umma_commit(&ctl.o_done[w]);
+                    }
+                }
+                if (one) umma_commit(&ctl.empty[slot]);
+                next();
             }
         }
         __syncwarp();
