@@ -156,11 +156,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
             for (int i = 0; i < st.n_tiles; ++i, ++it) {
                 const int tile = st.tile0 + i, slot = it % NST;
                 const int next = i + 1 < st.n_tiles ? page_of(tile + 1) : kNone;
-                if (it >= NST && live && !mbar_spin(&ctl.empty[slot], (it / NST - 1) & 1, a.wait_us)) {
+                if (!__all_sync(0xffffffffu, it < NST || mbar_spin(&ctl.empty[slot],
+                                                                   (it / NST - 1) & 1, a.wait_us))) {
                     live = false;
                     if (lane == 0) atomicOr(c.status, PROX_CACHE_TIMEOUT);
+                    break;
                 }
-                if (!live) break;
                 // a page id out of range: zeros (a box outside the map), and the mask
                 const bool wanted = page != kNone, good = page >= 0 && page < c.n_pages;
                 const unsigned bad = __ballot_sync(0xffffffffu, wanted && !good);
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
                 live = false;
                 if (lane == 0) atomicOr(c.status, PROX_CACHE_TIMEOUT);
             }
+            __syncwarp();  // (lanes may have seen the phase end at different tries)
             const uint32_t sk = smem_addr(sm) + slot * 2 * C::TILE, sv = sk + C::TILE;
             const uint32_t bad = ctl.bad[slot];
             // tiles with drafted or missing keys have rows of v that must not

@@ -15,9 +15,11 @@
 //            has grown by more than 2^8 since the offset in use was taken:
 //            e^(x - offset) <= 2^8 loses nothing in fp32 sums.
 //
-// One warp loads, one thread issues the MMAs, and four warps a row group do the
-// softmax. The next tile's scores are formed while this one's probabilities
-// are, so the softmax warps always have work; k and v are read once for 256 rows.
+// One warp loads, one thread issues the MMAs, and eight warps a row group do the
+// softmax: four take the even tiles (the first score buffer), four the odd ones,
+// so that one set forms probabilities while the other waits for scores or looks
+// for maxima. Both use one offset a row, which goes from tile to tile with a
+// token. k and v are read once for 256 rows.
 #include "attention.cuh"
 #include "umma.cuh"
 
@@ -40,7 +42,8 @@ struct Cfg {
     static constexpr int SLOTS = (210 * 1024 - NWG * QTILE) / TILE < kMaxSlots
                                      ? (210 * 1024 - NWG * QTILE) / TILE
                                      : kMaxSlots;
-    static constexpr int THREADS = 128 * NWG + 64;
+    static constexpr int SOFT = 256 * NWG;        // softmax threads
+    static constexpr int THREADS = SOFT + 64;
     static constexpr uint32_t COLS = NWG == 2 ? 512 : 256;  // tensor-memory columns
 };
 
@@ -50,8 +53,10 @@ static_assert(sizeof(Line) % 16 == 0, "barriers are 8-byte aligned");
 struct Ctl {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     // per row group: q written; scores there and probabilities there (two
-    // buffers); a tile's second product done
-    uint64_t q_ready[2], s_full[2][2], p_ready[2][2], o_done[2];
+    // buffers); a tile's second product done, and that of a stretch's last tile
+    uint64_t q_ready[2], s_full[2][2], p_ready[2][2], o_done[2], o_full[2];
+    uint64_t token[2][2][4];        // row group, set, warp: the row's offset is decided
+    float m[2][128], l[2][2][128];  // offsets in use (log2 units); a set's sums
     uint64_t poison[4];             // drafted tokens whose v has an infinity or NaN
     uint32_t tmem;
 };
@@ -174,13 +179,16 @@ __device__ __forceinline__ T uniform(T x) {
     return __shfl_sync(0xffffffffu, x, 0);
 }
 
-// bounded wait; once one has given up, later ones do not wait at all
+// bounded wait of a whole warp; once one has given up, later ones do not wait at
+// all. Lanes may see the phase end at different tries, and what follows (named
+// barriers, tensor-memory loads) wants the warp together again.
 __device__ __forceinline__ void wait_or_give_up(uint64_t *bar, uint32_t count, const AttnArgs &a,
                                                 bool &live) {
     if (live && !mbar_spin(bar, count & 1, a.wait_us)) {
         live = false;
         atomicOr(a.cache.status, PROX_CACHE_TIMEOUT);
     }
+    __syncwarp();
 }
 
 template <int D, int DT, int NWG>
@@ -196,7 +204,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
     Ctl &ctl = *reinterpret_cast<Ctl *>(&ln + 1);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const prox_cache &c = a.cache;
-    const int ps = c.page_size, G = a.n_heads / c.n_kv_heads;
+    const int ps = c.page_size, sh = 31 - __clz(ps), G = a.n_heads / c.n_kv_heads;
 
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
@@ -204,17 +212,19 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
             mbar_init(&ctl.empty[i], 1);
         }
         for (int w = 0; w < NWG; ++w) {
-            mbar_init(&ctl.q_ready[w], 4);
+            mbar_init(&ctl.q_ready[w], 8);
             mbar_init(&ctl.o_done[w], 1);
+            mbar_init(&ctl.o_full[w], 1);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&ctl.s_full[w][b], 1);
                 mbar_init(&ctl.p_ready[w][b], 4);
+                for (int q = 0; q < 4; ++q) mbar_init(&ctl.token[w][b][q], 1);
             }
         }
         mbar_fence_init();
     }
-    if (wid == 4 * NWG) tmem_alloc(&ctl.tmem, C::COLS);
-    if (wid == 4 * NWG + 1 && lane < 2)
+    if (wid == 8 * NWG) tmem_alloc(&ctl.tmem, C::COLS);
+    if (wid == 8 * NWG + 1 && lane < 2)
         asm volatile("prefetch.tensormap [%0];" ::"l"(
                          reinterpret_cast<uint64_t>(lane ? &a.map_v : &a.map_k))
                      : "memory");
@@ -231,7 +241,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
     const int per_box = min(ps, kKT), boxes = kKT / per_box;
     bool live = true;
 
-    if (wid == 4 * NWG + 1) {
+    if (wid == 8 * NWG + 1) {
         // ------------------------------------------------------------------
         // loading warp: lane = (page of the tile, 64 elements); the order of
         // slots is that of use: k0, k1, v0, k2, v1, ..., v last
@@ -245,12 +255,13 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
             const int32_t *table = c.page_table + (size_t)max(ln.seq[st.b], 0) * c.max_pages;
             auto page_of = [&](int tile) {
                 const int key = tile * kKT + pg * per_box;
-                return pg < boxes && key < tot ? table[key / ps] : kNone;
+                return pg < boxes && key < tot ? table[key >> sh] : kNone;
             };
             // one tile of k or v into the next slot
             auto load = [&](const CUtensorMap *map, int tile, int page) {
                 const int slot = it % SLOTS;
-                if (it >= SLOTS && !mbar_spin(&ctl.empty[slot], (it / SLOTS - 1) & 1, a.wait_us)) {
+                if (!__all_sync(0xffffffffu, it < SLOTS || mbar_spin(&ctl.empty[slot],
+                                                                     (it / SLOTS - 1) & 1, a.wait_us))) {
                     live = false;
                     if (lane == 0) atomicOr(c.status, PROX_CACHE_TIMEOUT);
                     return;
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                 // a page id out of range: zeros (a box outside the map), and the mask
                 const bool wanted = page != kNone, good = page_ok(c, page);
                 const unsigned load = __ballot_sync(0xffffffffu, wanted);
-                const int y = good ? (page * c.n_kv_heads + st.head) * ps + tile * kKT % ps
+                const int y = good ? (page * c.n_kv_heads + st.head) * ps + (tile * kKT & (ps - 1))
                                    : c.n_pages * c.n_kv_heads * ps;
                 if (wanted && !good) atomicOr(c.status, PROX_CACHE_BAD_STATE);
                 if (lane == 0)
@@ -285,7 +296,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
         if (!live)
             for (int k = max(0, it - SLOTS); k < it; ++k)
                 mbar_spin(&ctl.full[k % SLOTS], (k / SLOTS) & 1, 1000);
-    } else if (wid == 4 * NWG) {
+    } else if (wid == 8 * NWG) {
         // ------------------------------------------------------------------
         // the warp that issues the MMAs: one elected thread does, but the whole
         // warp runs the loops on values it knows to be uniform, so that operand
@@ -363,6 +374,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                                     hi | (v_lo + slot * (C::TILE >> 4) + k * (2048 >> 4)), pv_idesc,
                                     k > 0 || i > 0);
                         umma_commit(&ctl.o_done[w]);
+                        if (i + 1 == n_tiles) umma_commit(&ctl.o_full[w]);
                     }
                 }
                 if (one) umma_commit(&ctl.empty[slot]);
@@ -372,39 +384,43 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------------
-        // softmax: row group w, one thread a row
+        // softmax: set b of row group w, one thread a row
         // ------------------------------------------------------------------
-        const int w = wid >> 2, t = tid & 127;
+        const int w = wid >> 3, b = wid >> 2 & 1, t = tid & 127;
         const uint32_t lane_at = (uint32_t)(wid & 3) << 21;   // first tensor-memory lane << 16
-        const uint32_t to = t_o + w * 128 + lane_at;
+        const uint32_t ts = t_s + w * 128 + b * 64 + lane_at, to = t_o + w * 128 + lane_at;
         const float sc = a.scale * kLog2e;
-        uint32_t n_s = 0, n_o = 0;  // tiles of this row group so far
-        int it = 0;                 // slots used by the stretches so far
+        // tiles of the row group, of this set, tokens and stretches so far
+        uint32_t n = 0, mine = 0, n_tok = 0, n_full = 0;
+        int it = 0;                           // slots used by the stretches so far
         for (int pos = begin; pos < end;) {
             const Stretch st = stretch_at(ln, a, ROWS, pos, end);
             const bool first = pos == begin;
             pos += st.n_tiles;
             const int len = ln.len[st.b], tot = ln.tot[st.b];
             const int n_rows = ln.rows[st.b] * G - st.row_tile * ROWS;  // of this row tile
-            if (NWG == 2) named_bar_sync(2, 256);  // both groups are done with ctl.poison
+            named_bar_sync(2, C::SOFT);  // all are done with the last stretch's shared values
             if (w * 128 >= n_rows) {
                 it += 2 * st.n_tiles;
                 continue;
             }
-            if (w == 0 && t < 4) ctl.poison[t] = 0;
-            const bool there = tid < n_rows;             // (tid = w * 128 + t)
-            const bool busy = (wid * 32) < n_rows;       // the warp has rows
-            const int r = st.row_tile * ROWS + tid;
+            if (tid < 4) ctl.poison[tid] = 0;
+            const int rt = w * 128 + t;                  // row of the tile
+            const bool there = rt < n_rows;
+            const bool busy = rt - lane < n_rows;        // the warp has rows
+            const int r = st.row_tile * ROWS + rt;
             const int tok = there ? r / G : 0, head = st.head * G + (there ? r - tok * G : 0);
             const size_t row = ln.row0[st.b] + tok;
             const uint64_t *tree = a.tree ? a.tree + row * a.tree_words : nullptr;
             {
-                // q: 16-byte pieces; rows behind the last one are zeros
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * a.q_stride + (size_t)head * D);
+                // q: 16-byte pieces, every other one; rows behind the last one are zeros
+                const uint4 *src =
+                    reinterpret_cast<const uint4 *>(a.q + row * a.q_stride + (size_t)head * D);
                 unsigned char *dst = sq + w * C::QTILE + t * 128;
                 if (busy) {
 #pragma unroll
-                    for (int x = 0; x < D / 8; ++x) {
+                    for (int y = 0; y < D / 16; ++y) {
+                        const int x = 2 * y + b;
                         const uint4 v = there ? src[x] : make_uint4(0, 0, 0, 0);
                         *reinterpret_cast<uint4 *>(dst + (x >> 3) * C::QHALF +
                                                    (((x & 7) ^ (t & 7)) << 4)) = v;
@@ -415,21 +431,21 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.q_ready[w]);
             }
-            // pages of a tile with an id out of range, one bit each (the ids of the
-            // next tile are on their way while this one is worked on)
+            // pages of a tile with an id out of range, one bit each (the ids of this
+            // set's next tile are on their way while one is worked on)
             const int32_t *table = c.page_table + (size_t)max(ln.seq[st.b], 0) * c.max_pages;
-            auto peek = [&](int tile) {
-                const int key = tile * kKT + lane * per_box;
-                return lane < boxes && key < tot ? table[key / ps] : 0;
+            auto peek = [&](int i) {
+                const int key = (st.tile0 + i) * kKT + lane * per_box;
+                return i < st.n_tiles && lane < boxes && key < tot ? table[key >> sh] : 0;
             };
-            int page = peek(st.tile0);
-            float m = -INFINITY, l = 0.f;   // offset in use (log2 units) and sum
-            for (int i = 0; i < st.n_tiles; ++i) {
+            const int i0 = (n & 1) == b ? 0 : 1;  // this set's first tile
+            int page = peek(i0);
+            float m = -INFINITY, l = 0.f;         // offset that l counts from, and sum
+            for (int i = i0; i < st.n_tiles; i += 2) {
                 const int tile = st.tile0 + i;
                 const uint32_t bad = __ballot_sync(0xffffffffu, !page_ok(c, page));
-                page = i + 1 < st.n_tiles ? peek(tile + 1) : 0;
-                const uint32_t buf = n_s & 1, ts = t_s + w * 128 + buf * 64 + lane_at;
-                wait_or_give_up(&ctl.s_full[w][buf], n_s++ >> 1, a, live);
+                page = peek(i + 2);
+                wait_or_give_up(&ctl.s_full[w][b], mine++, a, live);
                 tc_fence_after();
                 const bool edge = (tile + 1) * kKT > len;
                 if (w == 0 && edge) {
@@ -470,86 +486,121 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                     fence_proxy_async_smem();
                 }
                 if (busy) {
-                    const bool masked = edge || bad;
                     uint64_t seen = ~0ull;
+                    const bool masked = edge || bad;
                     if (masked) {
-                        uint64_t ok = low_bits(tot - tile * kKT);
+                        seen = low_bits(tot - tile * kKT);
                         for (int p = 0; p < boxes; ++p)
-                            if (bad >> p & 1) ok &= ~(low_bits(per_box) << (p * per_box));
-                        seen = there ? seen_bits(tree, a.tree_words, len, tok, tile * kKT) & ok : 0ull;
+                            if (bad >> p & 1) seen &= ~(low_bits(per_box) << (p * per_box));
+                        seen = there ? seen_bits(tree, a.tree_words, len, tok, tile * kKT) & seen : 0ull;
                     }
-                    uint32_t s[kKT], p[kKT / 2];
-                    tmem_ask32(ts, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-                    tmem_ask32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-                    tmem_take32(*reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-                    tmem_take32(*reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-                    if (masked) {
+                    // 32 scores; those not seen are -inf
+                    auto scores = [&](int q, uint32_t(&s)[32]) {
+                        tmem_get32(ts + q * 32, s);
+                        if (masked) {
+                            const uint32_t bits = (uint32_t)(seen >> q * 32);
 #pragma unroll
-                        for (int x = 0; x < kKT; ++x)
-                            if (!(seen >> x & 1)) s[x] = 0xff800000u;
-                    }
+                            for (int x = 0; x < 32; ++x)
+                                if (!(bits >> x & 1)) s[x] = 0xff800000u;
+                        }
+                    };
+                    // (read twice: 96 registers a thread do not hold 64 of them)
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int x = 0; x < kKT; ++x)
-                        mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+                    for (int q = 0; q < kKT / 32; ++q) {
+                        uint32_t s[32];
+                        scores(q, s);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+                    }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                    if (__any_sync(0xffffffffu, top > m + kGrow || (top > m && m == -INFINITY))) {
-                        const float nm = fmaxf(m, top);
-                        const float f = nm > m ? ex2(m - nm) : 1.f;
-                        m = nm;
-                        l *= f;
+                    // the offset that the tiles before this one left, and this one's
+                    float now = -INFINITY;
+                    if (i > 0) {
+                        wait_or_give_up(&ctl.token[w][b][wid & 3], n_tok++, a, live);
+                        now = ctl.m[w][t];
+                    }
+                    if (__any_sync(0xffffffffu, top > now + kGrow || (top > now && now == -INFINITY))) {
+                        const float nm = fmaxf(now, top);
+                        const float f = nm > now ? ex2(now - nm) : 1.f;
+                        now = nm;
                         if (i > 0) {
-                            // (products up to the last tile's are in the outputs)
-                            wait_or_give_up(&ctl.o_done[w], n_o - 1, a, live);
+                            // Products up to the last tile's are in the outputs then. (A
+                            // wait tells a phase by its parity: tile i's scores were
+                            // formed behind the product of tile i - 2, and tile i's own
+                            // product waits for this thread, so it is the phase of tile
+                            // i - 1 or the one behind it that is under way.)
+                            wait_or_give_up(&ctl.o_done[w], n + i - 1, a, live);
                             tc_fence_after();
 #pragma unroll 1
-                            for (int q = 0; q < D / 32; ++q) {
-                                uint32_t o[32];
-                                tmem_get32(to + q * 32, o);
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t o[16];
+                                tmem_ld16(to + q * 16, o);
 #pragma unroll
-                                for (int x = 0; x < 32; ++x)
+                                for (int x = 0; x < 16; ++x)
                                     o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                                tmem_st16(to + q * 32, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-                                tmem_st16(to + q * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+                                tmem_st16(to + q * 16, o);
                             }
                         }
+                    }
+                    ctl.m[w][t] = now;
+                    __syncwarp();
+                    if (lane == 0 && i + 1 < st.n_tiles) mbar_arrive(&ctl.token[w][b ^ 1][wid & 3]);
+                    if (now > m) {
+                        l *= ex2(m - now);
+                        m = now;
                     }
                     const float mu = m == -INFINITY ? 0.f : m;
                     const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int x = 0; x < kKT; x += 2) {
-                        const float2 z = fma2(
-                            make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), sc2, mu2);
-                        const float2 e = make_float2(ex2(z.x), ex2(z.y));
-                        sum[x / 2 & 1] = add2(sum[x / 2 & 1], e);
-                        p[x / 2] = pack2<DT>(e.x, e.y);
+                    for (int q = 0; q < kKT / 32; ++q) {
+                        uint32_t s[32], p[16];
+                        scores(q, s);
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) {
+                            const float2 z = fma2(
+                                make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), sc2, mu2);
+                            const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                            sum[x / 2 & 1] = add2(sum[x / 2 & 1], e);
+                            p[x / 2] = pack2<DT>(e.x, e.y);
+                        }
+                        tmem_st16(ts + q * 16, p);
                     }
                     sum[0] = add2(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
-#pragma unroll
-                    for (int q = 0; q < kKT / 32; ++q)
-                        tmem_st16(ts + q * 16, *reinterpret_cast<uint32_t(*)[16]>(&p[q * 16]));
                     tmem_st_wait();
                 }
-                ++n_o;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_ready[w][buf]);
+                if (lane == 0) mbar_arrive(&ctl.p_ready[w][b]);
             }
             it += 2 * st.n_tiles;
+            n += st.n_tiles;
             // --------------------------------------------------------------
-            // the rows' outputs, or a piece of them
+            // the rows' outputs, or a piece of them: each set half the columns
             // --------------------------------------------------------------
-            wait_or_give_up(&ctl.o_done[w], n_o - 1, a, live);
+            wait_or_give_up(&ctl.o_full[w], n_full++, a, live);
             tc_fence_after();
+            named_bar_sync(3 + w, 256);
             if (busy) {
+                // the last offset is the one of the last tile's set; the other set's
+                // sum counts from what it last saw
+                const float last = ctl.m[w][t];
+                ctl.l[w][b][t] = m == -INFINITY ? 0.f : l * ex2(m - last);
+                __syncwarp();
+            }
+            named_bar_sync(3 + w, 256);
+            if (busy) {
+                m = ctl.m[w][t];
+                l = ctl.l[w][0][t] + ctl.l[w][1][t];
                 const bool whole = st.n_tiles == st.all_tiles;
                 const float inv = l == 0.f ? 0.f : whole ? 1.f / l : 1.f;
                 float *part = piece(a, blockIdx.x, first, D, ROWS);
                 const uint64_t any = ctl.poison[0] | ctl.poison[1] | ctl.poison[2] | ctl.poison[3];
 #pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
+                for (int q = b * (D / 64); q < (b + 1) * (D / 64); ++q) {
                     uint32_t ob[32];
                     tmem_get32(to + q * 32, ob);
                     float o[32];
@@ -563,11 +614,12 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                             for (; bits; bits &= bits - 1) {
                                 const int key = len + k * 64 + __ffsll((long long)bits) - 1;
                                 const int page =
-                                    c.page_table[(size_t)ln.seq[st.b] * c.max_pages + key / ps];
+                                    c.page_table[(size_t)ln.seq[st.b] * c.max_pages + (key >> sh)];
                                 if (!page_ok(c, page)) continue;  // (cannot be: its box was read)
                                 const uint32_t *v = reinterpret_cast<const uint32_t *>(
                                     a.v_layer +
-                                    (((size_t)page * c.n_kv_heads + st.head) * ps + key % ps) * D + q * 32);
+                                    (((size_t)page * c.n_kv_heads + st.head) * ps + (key & (ps - 1))) * D +
+                                    q * 32);
 #pragma unroll
                                 for (int x = 0; x < 32; x += 2) {
                                     const uint32_t vv = v[x / 2];
@@ -582,7 +634,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                     if (!whole) {
 #pragma unroll
                         for (int x = 0; x < 32; x += 4)
-                            reinterpret_cast<float4 *>(part)[(size_t)(q * 8 + x / 4) * ROWS + tid] =
+                            reinterpret_cast<float4 *>(part)[(size_t)(q * 8 + x / 4) * ROWS + rt] =
                                 make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
                     } else if (there) {
                         uint4 *op = reinterpret_cast<uint4 *>(a.out + row * a.out_stride +
@@ -594,10 +646,10 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
                                                    pack2<DT>(o[x + 6], o[x + 7]));
                     }
                 }
-                if (!whole) {
-                    part[ROWS * D + tid] = m;
-                    part[ROWS * (D + 1) + tid] = l;
-                } else if (there && a.lse) {
+                if (b == 0 && !whole) {
+                    part[ROWS * D + rt] = m;
+                    part[ROWS * (D + 1) + rt] = l;
+                } else if (b == 0 && there && a.lse) {
                     a.lse[row * a.n_heads + head] =
                         m == -INFINITY && l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
@@ -606,7 +658,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
         }
     }
     __syncthreads();
-    if (wid == 4 * NWG) tmem_free(tmem, C::COLS);
+    if (wid == 8 * NWG) tmem_free(tmem, C::COLS);
 }
 
 template <int D, int DT, int NWG>
