@@ -658,7 +658,7 @@ struct Plan {
 Plan plan_of(int max_rows) {
     if (max_rows <= 16) return {16, 2, false};
     if (max_rows <= 32) return {32, 2, false};
-    if (max_rows <= 128) return {128, 1, true};
+    if (max_rows <= 128) return {128, 2, true};
     return {256, 1, true};
 }
 

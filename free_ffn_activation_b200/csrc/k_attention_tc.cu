@@ -38,10 +38,13 @@ struct Cfg {
     static constexpr int HALF = kKT * 128;        // bytes of one of them, of a tile of k (or v)
     static constexpr int TILE = HALF * H;         // bytes of a tile of k (or v)
     static constexpr int QHALF = 128 * 128, QTILE = QHALF * H;  // the same of a group's q
-    // slots of the ring: what fits beside q in 210 KB
-    static constexpr int SLOTS = (210 * 1024 - NWG * QTILE) / TILE < kMaxSlots
-                                     ? (210 * 1024 - NWG * QTILE) / TILE
-                                     : kMaxSlots;
+    // one CTA of two row groups fills an SM's tensor memory; of one row group,
+    // two CTAs do
+    static constexpr int PER_SM = 3 - NWG;
+    // slots of the ring: what fits beside q
+    static constexpr int ROOM = (NWG == 2 ? 210 : 102) * 1024;
+    static constexpr int SLOTS =
+        (ROOM - NWG * QTILE) / TILE < kMaxSlots ? (ROOM - NWG * QTILE) / TILE : kMaxSlots;
     static constexpr int SOFT = 256 * NWG;        // softmax threads
     static constexpr int THREADS = SOFT + 64;
     static constexpr uint32_t COLS = NWG == 2 ? 512 : 256;  // tensor-memory columns
@@ -192,7 +195,7 @@ __device__ __forceinline__ void wait_or_give_up(uint64_t *bar, uint32_t count, c
 }
 
 template <int D, int DT, int NWG>
-__global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
     k_attention_tc(const __grid_constant__ AttnArgs a) {
     using C = Cfg<D, NWG>;
     constexpr int ROWS = C::ROWS, H = C::H, SLOTS = C::SLOTS;
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, 1)
 template <int D, int DT, int NWG>
 cudaError_t run(const AttnArgs &a, cudaStream_t s) {
     constexpr size_t smem = smem_bytes<D, NWG>();
-    static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+    static_assert(Cfg<D, NWG>::PER_SM * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
     auto kern = k_attention_tc<D, DT, NWG>;
     cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;
