@@ -1,11 +1,12 @@
 // Page operations of the paged key/value cache (include/prox_decode.h).
 //
-// Bookkeeping (reserve, fork, free) runs in one cluster of eight CTAs: the
+// Bookkeeping (reserve, fork, free) runs in one cluster of CTAs: the
 // entries' page counts are prefix-summed by every CTA for itself, so each
 // entry's place on the free list is known without atomics and the result does
 // not depend on timing, and the pages are then handled in chunks of 32 columns
-// dealt out to the cluster's warps. Decisions are taken from the state before
-// the call; a cluster barrier separates these reads from the first write.
+// dealt out to the cluster's warps. Decisions are taken from lengths, page
+// counts and the free count, which are written behind a cluster barrier only.
+// These kernels are bound by latency: a chain of dependent reads and barriers.
 // The rows themselves are moved by kernels over the whole GPU (fork's copies,
 // append, compact), a warp or a group of lanes per run of rows.
 #include "decode_internal.cuh"
@@ -13,20 +14,27 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <cstdint>
+#include <mutex>
+#include <set>
+#include <utility>
 
 namespace cg = cooperative_groups;
 
 namespace prox {
 namespace {
 
-constexpr int kCl = 8;                 // CTAs of the bookkeeping cluster (portable size)
-constexpr int kBkThreads = 1024;
-constexpr int kBkWarps = kBkThreads / 32;
-constexpr int kPerThread = kMaxSeqs / kBkThreads;
+// Shapes of a bookkeeping call: few entries that can list few pages (by the page
+// table's width) run on 8 CTAs of 256 threads, others on 16 of 1024. Fork and
+// free of 8 sequences of 50 pages: 16 against 19 us; of 32 of 2,500: 138 against
+// 41 us.
+constexpr int kFew = 256, kFewPages = 1 << 14, kFewCtas = 8;
+constexpr int kSome = 1024, kCtas = 16;
+constexpr int kWindow = 8192;          // chunks of a CTA whose owners and masks are kept
 
 // exclusive prefix sum over the block (and the total), v per thread
-template <typename T>
+template <int THREADS, typename T>
 __device__ T block_scan(T v, T *tmp, T *total) {
+    constexpr int WARPS = THREADS / 32;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     T x = v;
 #pragma unroll
@@ -37,33 +45,33 @@ __device__ T block_scan(T v, T *tmp, T *total) {
     __syncthreads();
     if (lane == 31) tmp[wid] = x;
     __syncthreads();
-    if (wid == 0) {
-        T w = tmp[lane];
+    // every warp sums the warps for itself
+    T w = lane < WARPS ? tmp[lane] : T(0);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const T y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        tmp[lane] = w;
+    for (int o = 1; o < WARPS; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
     }
-    __syncthreads();
-    const T base = wid ? tmp[wid - 1] : T(0);
-    *total = tmp[31];
-    return base + x - v;
+    *total = __shfl_sync(0xffffffffu, w, WARPS - 1);
+    const T base = __shfl_sync(0xffffffffu, w, wid ? wid - 1 : 0);
+    return (wid ? base : T(0)) + x - v;
 }
 
-// shared memory of a bookkeeping CTA: `first` finds sequences listed twice,
-// the others hold what each entry needs
+// shared memory of a bookkeeping CTA of N entries at most: `first` finds
+// sequences listed twice, the others hold what each entry needs
+template <int N>
 struct Book {
-    int first[kMaxSeqs];       // lowest entry that lists the sequence
-    int seq[kMaxSeqs];         // sequence of the entry, -1 = left out
-    int aux[kMaxSeqs];         // fork: source; reserve: columns held so far
-    int cols[kMaxSeqs];        // columns (pages) the entry works on
-    int base[kMaxSeqs];        // pages taken by the entries before it
-    int chunk[kMaxSeqs + 1];   // chunks of 32 columns before it
+    int seq[N];          // sequence of the entry, -1 = left out
+    int aux[N];          // fork: source; reserve: columns held so far
+    int len[N];          // fork: the source's length
+    int cols[N];         // columns (pages) the entry works on
+    int base[N];         // pages taken by the entries before it
+    int chunk[N + 1];    // chunks of 32 columns before it
     int tmp[32];
     long long wide[32];
-    int count;                 // free: pages given back by this CTA
+    int count;           // free: pages given back by this CTA
+    int odd;             // free: a count was 0 already
+    int first[kMaxSeqs]; // lowest entry that lists the sequence (max_seqs of them)
 };
 
 // entry whose chunks contain chunk c: the last i with chunk[i] <= c
@@ -80,24 +88,28 @@ __device__ __forceinline__ int find_entry(const int *chunk, int n, int c) {
 }
 
 // marks each sequence's first listing (all threads; ends with a barrier)
-__device__ void find_first(const prox_cache &c, Book &b, const int32_t *seqs, int n) {
-    for (int s = threadIdx.x; s < c.max_seqs; s += kBkThreads) b.first[s] = 0x7fffffff;
+template <int THREADS>
+__device__ void find_first(const prox_cache &c, int *first, const int32_t *seqs, int n) {
+    for (int s = threadIdx.x; s < c.max_seqs; s += THREADS) first[s] = 0x7fffffff;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kBkThreads) {
+    for (int i = threadIdx.x; i < n; i += THREADS) {
         const int s = seqs[i];
-        if (s >= 0 && s < c.max_seqs) atomicMin(&b.first[s], i);
+        if (s >= 0 && s < c.max_seqs) atomicMin(&first[s], i);
     }
     __syncthreads();
 }
 
 // exclusive sums of chunks of 32 columns over the entries; returns their count
-__device__ int sum_chunks(Book &b, int n) {
-    const int i0 = threadIdx.x * kPerThread;
+// (ends with a barrier)
+template <int THREADS, int N>
+__device__ int sum_chunks(Book<N> &b, int n) {
+    constexpr int PER = N / THREADS;
+    const int i0 = threadIdx.x * PER;
     int mine = 0, total;
-    for (int k = 0; k < kPerThread; ++k)
+    for (int k = 0; k < PER; ++k)
         if (i0 + k < n) mine += (b.cols[i0 + k] + 31) >> 5;
-    int at = block_scan(mine, b.tmp, &total);
-    for (int k = 0; k < kPerThread; ++k)
+    int at = block_scan<THREADS>(mine, b.tmp, &total);
+    for (int k = 0; k < PER; ++k)
         if (i0 + k < n) {
             b.chunk[i0 + k] = at;
             at += (b.cols[i0 + k] + 31) >> 5;
@@ -110,19 +122,22 @@ __device__ int sum_chunks(Book &b, int n) {
 // others as long as the sum up to and with them fits in the free list. need
 // comes from `need_of(i)` (-1: refused for another reason). base[] gets the
 // pages taken before the entry; returns the pages taken in all.
-template <typename F>
-__device__ int take_pages(Book &b, int n, int n_free, uint32_t *status, bool *fits, F need_of) {
+template <int THREADS, int N, typename F>
+__device__ int take_pages(Book<N> &b, int n, int n_free, uint32_t *status, bool *fits, F need_of) {
     // (sums in 64 bits: refused entries may ask for more pages than there are)
-    const int i0 = threadIdx.x * kPerThread;
-    int need[kPerThread];
+    constexpr int PER = N / THREADS;
+    const int i0 = threadIdx.x * PER;
+    int need[PER];
     long long mine = 0, total;
-    for (int k = 0; k < kPerThread; ++k) {
+    for (int k = 0; k < PER; ++k) {
         need[k] = i0 + k < n ? need_of(i0 + k) : -1;
         mine += max(need[k], 0);
     }
-    long long at = block_scan(mine, b.wide, &total);
+    long long at = block_scan<THREADS>(mine, b.wide, &total);
+    if (threadIdx.x == 0) b.count = 0;
+    __syncthreads();
     int taken = 0;
-    for (int k = 0; k < kPerThread; ++k) {
+    for (int k = 0; k < PER; ++k) {
         if (i0 + k >= n) continue;
         const bool ok = need[k] == 0 || (need[k] > 0 && at + need[k] <= n_free);
         b.base[i0 + k] = ok ? (int)min(at, (long long)n_free) : 0;
@@ -136,16 +151,10 @@ __device__ int take_pages(Book &b, int n, int n_free, uint32_t *status, bool *fi
         }
     }
     // entries that fit and need pages come first: the largest end is the sum
-    int best = taken;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    taken = __reduce_max_sync(0xffffffffu, taken);
+    if ((threadIdx.x & 31) == 0 && taken > 0) atomicMax(&b.count, taken);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) b.tmp[threadIdx.x >> 5] = best;
-    __syncthreads();
-    best = 0;
-    for (int w = 0; w < kBkWarps; ++w) best = max(best, b.tmp[w]);
-    __syncthreads();
-    return best;
+    return b.count;
 }
 
 __device__ __forceinline__ int free_count(const prox_cache &c) {
@@ -184,19 +193,20 @@ __global__ void __launch_bounds__(256) k_cache_init(const prox_cache c) {
 // ---------------------------------------------------------------------------
 // reserve
 // ---------------------------------------------------------------------------
-__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
+template <int THREADS, int N>
+__global__ void __launch_bounds__(THREADS)
     k_cache_reserve(const prox_cache c, int n, const int32_t *seqs, const int32_t *n_new,
                     uint8_t *ok_out) {
     extern __shared__ __align__(16) unsigned char smem[];
-    Book &b = *reinterpret_cast<Book *>(smem);
+    Book<N> &b = *reinterpret_cast<Book<N> *>(smem);
     cg::cluster_group cl = cg::this_cluster();
     const int rank = cl.block_rank();
     pdl_wait();
     pdl_launch();
     const int n_free = free_count(c);
-    find_first(c, b, seqs, n);
-    bool fits[kPerThread];
-    const int taken = take_pages(b, n, n_free, c.status, fits, [&](int i) {
+    find_first<THREADS>(c, b.first, seqs, n);
+    bool fits[N / THREADS];
+    const int taken = take_pages<THREADS>(b, n, n_free, c.status, fits, [&](int i) {
         const int s = entry_seq(c, seqs, i);
         b.seq[i] = -1;
         b.cols[i] = 0;
@@ -221,8 +231,8 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
         b.cols[i] = max(0, (int)want - st.held);
         return b.cols[i];
     });
-    for (int k = 0; k < kPerThread; ++k) {
-        const int i = threadIdx.x * kPerThread + k;
+    for (int k = 0; k < N / THREADS; ++k) {
+        const int i = threadIdx.x * (N / THREADS) + k;
         if (i >= n) continue;
         if (!fits[k]) {
             b.seq[i] = -1;
@@ -230,19 +240,18 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
         }
         if (rank == 0 && ok_out) ok_out[i] = fits[k] ? 1 : 0;
     }
-    __syncthreads();
-    const int chunks = sum_chunks(b, n);
-    cl.sync();  // every CTA has read the state
+    const int chunks = sum_chunks<THREADS>(b, n);
     const int lane = threadIdx.x & 31;
-    for (int q = rank * kBkWarps + (threadIdx.x >> 5); q < chunks; q += kCl * kBkWarps) {
+    for (int q = rank * (THREADS / 32) + (threadIdx.x >> 5); q < chunks; q += cl.num_blocks() * (THREADS / 32)) {
         const int i = find_entry(b.chunk, n, q);
         const int j = (q - b.chunk[i]) * 32 + lane;
         if (j >= b.cols[i]) continue;
         c.page_table[(size_t)b.seq[i] * c.max_pages + b.aux[i] + j] =
             pop_page(c, n_free, b.base[i] + j);
     }
+    cl.sync();  // every CTA has read the state
     if (rank == 0) {
-        for (int i = threadIdx.x; i < n; i += kBkThreads)
+        for (int i = threadIdx.x; i < n; i += THREADS)
             if (b.seq[i] >= 0 && b.cols[i] > 0) c.held[b.seq[i]] = b.aux[i] + b.cols[i];
         if (threadIdx.x == 0) *c.n_free = n_free - taken;
     }
@@ -252,21 +261,20 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
 // fork
 // ---------------------------------------------------------------------------
 // ws: [0] = page copies, then {source page, target page, rows, -} for each
-__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
+template <int THREADS, int N>
+__global__ void __launch_bounds__(THREADS)
     k_cache_fork(const prox_cache c, int n, const int32_t *src, const int32_t *dst, int share,
                  uint8_t *ok_out, int32_t *ws) {
     extern __shared__ __align__(16) unsigned char smem[];
-    Book &b = *reinterpret_cast<Book *>(smem);
+    Book<N> &b = *reinterpret_cast<Book<N> *>(smem);
     cg::cluster_group cl = cg::this_cluster();
     const int rank = cl.block_rank(), ps = c.page_size;
     pdl_wait();
     pdl_launch();
     const int n_free = free_count(c);
-    find_first(c, b, dst, n);
-    bool fits[kPerThread];
-    int len[kPerThread];
-    const int taken = take_pages(b, n, n_free, c.status, fits, [&](int i) {
-        const int k = i - threadIdx.x * kPerThread;
+    find_first<THREADS>(c, b.first, dst, n);
+    bool fits[N / THREADS];
+    const int taken = take_pages<THREADS>(b, n, n_free, c.status, fits, [&](int i) {
         const int d = entry_seq(c, dst, i), s = entry_seq(c, src, i);
         b.seq[i] = -1;
         b.cols[i] = 0;
@@ -276,18 +284,19 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
             return -1;
         }
         if (s < 0) return -1;
-        if (c.length[d] != 0 || c.held[d] != 0) {
+        const int dl = c.length[d], dh = c.held[d], l = seq_state(c, s).len;
+        if (dl != 0 || dh != 0) {
             atomicOr(c.status, PROX_CACHE_BAD_ARG);
             return -1;
         }
-        len[k] = seq_state(c, s).len;
         b.seq[i] = d;
         b.aux[i] = s;
-        b.cols[i] = (len[k] + ps - 1) / ps;
-        return share ? (len[k] % ps ? 1 : 0) : b.cols[i];
+        b.len[i] = l;
+        b.cols[i] = (l + ps - 1) / ps;
+        return share ? (l % ps ? 1 : 0) : b.cols[i];
     });
-    for (int k = 0; k < kPerThread; ++k) {
-        const int i = threadIdx.x * kPerThread + k;
+    for (int k = 0; k < N / THREADS; ++k) {
+        const int i = threadIdx.x * (N / THREADS) + k;
         if (i >= n) continue;
         if (!fits[k]) {
             b.seq[i] = -1;
@@ -295,41 +304,51 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
         }
         if (rank == 0 && ok_out) ok_out[i] = fits[k] ? 1 : 0;
     }
-    __syncthreads();
-    const int chunks = sum_chunks(b, n);
-    cl.sync();  // every CTA has read the state
+    const int chunks = sum_chunks<THREADS>(b, n);
     const int lane = threadIdx.x & 31;
-    for (int q = rank * kBkWarps + (threadIdx.x >> 5); q < chunks; q += kCl * kBkWarps) {
-        const int i = find_entry(b.chunk, n, q);
-        const int j = (q - b.chunk[i]) * 32 + lane;
-        if (j >= b.cols[i]) continue;
-        const int l = min(max(c.length[b.aux[i]], 0), b.cols[i] * ps);
-        const int rows = min(ps, l - j * ps);
-        int p = c.page_table[(size_t)b.aux[i] * c.max_pages + j];
-        const bool good = page_ok(c, p);
-        if (!good) atomicOr(c.status, PROX_CACHE_BAD_STATE);
-        if (share && rows == ps) {
-            if (good) atomicAdd(&c.ref_count[p], 1);
-        } else {
-            const int k = b.base[i] + (share ? 0 : j);
-            const int to = pop_page(c, n_free, k);
-            int4 copy = make_int4(p, to, good && to >= 0 ? rows : 0, 0);
-            reinterpret_cast<int4 *>(ws + 4)[k] = copy;
-            p = to;
+    // two chunks a step, their reads in flight together
+    constexpr int U = 2;
+    const int step = (int)cl.num_blocks() * (THREADS / 32);
+    for (int q0 = rank * (THREADS / 32) + (threadIdx.x >> 5); q0 < chunks; q0 += step * U) {
+        int at[U], col[U], page[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = q0 + u * step;
+            at[u] = q < chunks ? find_entry(b.chunk, n, q) : -1;
+            if (at[u] >= 0) {
+                col[u] = (q - b.chunk[at[u]]) * 32 + lane;
+                if (col[u] >= b.cols[at[u]]) at[u] = -1;
+            }
+            if (at[u] >= 0)
+                page[u] = c.page_table[(size_t)b.aux[at[u]] * c.max_pages + col[u]];
         }
-        c.page_table[(size_t)b.seq[i] * c.max_pages + j] = p;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = at[u], j = col[u];
+            if (i < 0) continue;
+            const int rows = min(ps, b.len[i] - j * ps);
+            int p = page[u];
+            const bool good = page_ok(c, p);
+            if (!good) atomicOr(c.status, PROX_CACHE_BAD_STATE);
+            if (share && rows == ps) {
+                if (good) atomicAdd(&c.ref_count[p], 1);
+            } else {
+                const int k = b.base[i] + (share ? 0 : j);
+                const int to = pop_page(c, n_free, k);
+                const int4 copy = make_int4(p, to, good && to >= 0 ? rows : 0, 0);
+                reinterpret_cast<int4 *>(ws + 4)[k] = copy;
+                p = to;
+            }
+            c.page_table[(size_t)b.seq[i] * c.max_pages + j] = p;
+        }
     }
-    // a target's length is written once its columns are: sources were read above
-    // by warps of every CTA, and no target with a length is a source of this call
-    cl.sync();
+    cl.sync();  // every CTA has read the state
     if (rank == 0) {
-        for (int k = 0; k < kPerThread; ++k) {
-            const int i = threadIdx.x * kPerThread + k;
-            if (i < n && b.seq[i] >= 0) {
-                c.length[b.seq[i]] = len[k];
+        for (int i = threadIdx.x; i < n; i += THREADS)
+            if (b.seq[i] >= 0) {
+                c.length[b.seq[i]] = b.len[i];
                 c.held[b.seq[i]] = b.cols[i];
             }
-        }
         if (threadIdx.x == 0) {
             *c.n_free = n_free - taken;
             ws[0] = taken;
@@ -386,17 +405,29 @@ __global__ void __launch_bounds__(256) k_cache_copy(const prox_cache c, const in
 constexpr int kClaim = (int)0x80000000;      // + listing number < 2^30
 constexpr int kClaimEnd = kClaim + (1 << 30);
 
-__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
+// A CTA's chunks are a run, so that pages come out in listing order. Which entry
+// a chunk belongs to and which of its lanes push their page is kept for a window
+// of chunks (all of them, up to two million pages a call).
+struct Window {
+    uint16_t owner[kWindow];
+    uint32_t mask[kWindow];
+    int before[kWindow];
+};
+
+template <int THREADS, int N>
+__global__ void __launch_bounds__(THREADS)
     k_cache_free(const prox_cache c, int n, const int32_t *seqs) {
     extern __shared__ __align__(16) unsigned char smem[];
-    Book &b = *reinterpret_cast<Book *>(smem);
+    Book<N> &b = *reinterpret_cast<Book<N> *>(smem);
+    Window &w = *reinterpret_cast<Window *>(smem + (sizeof(Book<N>) + 15) / 16 * 16);
     cg::cluster_group cl = cg::this_cluster();
     const int rank = cl.block_rank();
+    constexpr int WARPS = THREADS / 32, U = 4;
     pdl_wait();
     pdl_launch();
     const int n_free = free_count(c);
-    find_first(c, b, seqs, n);
-    for (int i = threadIdx.x; i < n; i += kBkThreads) {
+    find_first<THREADS>(c, b.first, seqs, n);
+    for (int i = threadIdx.x; i < n; i += THREADS) {
         int s = entry_seq(c, seqs, i);
         b.cols[i] = 0;
         if (s >= 0 && b.first[s] != i) {
@@ -406,15 +437,19 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
         if (s >= 0) b.cols[i] = seq_state(c, s).held;
         b.seq[i] = s;
     }
+    if (threadIdx.x == 0) b.odd = 0;
     __syncthreads();
-    const int chunks = sum_chunks(b, n);
-    // each CTA owns a run of chunks, so that pages come out in listing order
-    const int per = (chunks + kCl - 1) / kCl;
+    const int chunks = sum_chunks<THREADS>(b, n);
+    const int ctas = cl.num_blocks(), per = (chunks + ctas - 1) / ctas;
     const int q0 = min(rank * per, chunks), q1 = min(q0 + per, chunks);
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const bool kept = q1 - q0 <= kWindow;
+    for (int q = q0 + threadIdx.x; kept && q < q1; q += THREADS)
+        w.owner[q - q0] = (uint16_t)find_entry(b.chunk, n, q);
+    __syncthreads();
     auto page_at = [&](int q) {  // this lane's page of chunk q, -1 = none
         if (q >= q1) return -1;
-        const int i = find_entry(b.chunk, n, q);
+        const int i = kept ? w.owner[q - q0] : find_entry(b.chunk, n, q);
         const int j = (q - b.chunk[i]) * 32 + lane;
         if (j >= b.cols[i]) return -1;
         const int p = c.page_table[(size_t)b.seq[i] * c.max_pages + j];
@@ -422,64 +457,91 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kBkThreads)
         atomicOr(c.status, PROX_CACHE_BAD_STATE);
         return -1;
     };
-    for (int q = q0 + wid; q < q1; q += kBkWarps) {
-        const int p = page_at(q);
+    // the CTA's pages, U chunks a warp in flight; f(chunk, page of this lane or -1)
+    auto each = [&](int from, int to, auto f) {
+        for (int q = from + wid; q < to; q += WARPS * U) {
+            int p[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) p[u] = q + u * WARPS < to ? page_at(q + u * WARPS) : -1;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (q + u * WARPS < to) f(q + u * WARPS, p[u]);
+        }
+    };
+    each(q0, q1, [&](int, int p) {
         // a count that was 0 or less belongs to a page that is free already
-        if (p >= 0 && atomicSub(&c.ref_count[p], 1) <= 0) atomicOr(c.status, PROX_CACHE_BAD_STATE);
-    }
+        if (p >= 0 && atomicSub(&c.ref_count[p], 1) <= 0) {
+            atomicOr(c.status, PROX_CACHE_BAD_STATE);
+            b.odd = 1;
+        }
+    });
     __threadfence();
     cl.sync();
-    for (int q = q0 + wid; q < q1; q += kBkWarps) {
-        const int p = page_at(q);
-        if (p < 0) continue;
+    each(q0, q1, [&](int q, int p) {
+        if (p < 0) return;
         const int r = __ldcg(&c.ref_count[p]);
         if (r == 0 || r < kClaimEnd) atomicMin(&c.ref_count[p], kClaim + q * 32 + lane);
-    }
+    });
     __threadfence();
     cl.sync();
+    // pages this CTA pushes; their masks stay if all of its chunks are kept
+    if (threadIdx.x == 0) b.count = 0;
+    __syncthreads();
     int mine = 0;
-    for (int q = q0 + wid; q < q1; q += kBkWarps) {
-        const int p = page_at(q);
+    each(q0, q1, [&](int q, int p) {
         const bool won = p >= 0 && __ldcg(&c.ref_count[p]) == kClaim + q * 32 + lane;
-        mine += __popc(__ballot_sync(0xffffffffu, won));
-    }
-    int total;
-    block_scan(lane == 0 ? mine : 0, b.tmp, &total);
-    if (threadIdx.x == 0) b.count = total;
+        const unsigned m = __ballot_sync(0xffffffffu, won);
+        mine += __popc(m);
+        if (kept && lane == 0) w.mask[q - q0] = m;
+    });
+    if (lane == 0 && mine) atomicAdd(&b.count, mine);
     cl.sync();
     int at = n_free, all = n_free;
-    for (int r = 0; r < kCl; ++r) {
+    for (int r = 0; r < ctas; ++r) {
         const int k = *cl.map_shared_rank(&b.count, r);
         if (r < rank) at += k;
         all += k;
     }
-    for (int q = q0; q < q1; q += kBkWarps) {
-        const int p = page_at(q + wid);
-        const int code = kClaim + (q + wid) * 32 + lane;
-        const bool won = p >= 0 && __ldcg(&c.ref_count[p]) == code;
-        const unsigned m = __ballot_sync(0xffffffffu, won);
-        int sum;
-        const int before = block_scan(lane == 0 ? __popc(m) : 0, b.tmp, &sum);
-        const int pos = at + __shfl_sync(0xffffffffu, before, 0) + __popc(m & ((1u << lane) - 1));
-        if (won) {
+    for (int from = q0; from < q1; from += kWindow) {
+        const int to = min(from + kWindow, q1);
+        if (!kept) {
+            each(from, to, [&](int q, int p) {
+                const bool won = p >= 0 && __ldcg(&c.ref_count[p]) == kClaim + q * 32 + lane;
+                const unsigned m = __ballot_sync(0xffffffffu, won);
+                if (lane == 0) w.mask[q - from] = m;
+            });
+            __syncthreads();
+        }
+        // places of the window's chunks: each thread sums a run of them
+        const int run = (to - from + THREADS - 1) / THREADS, k0 = threadIdx.x * run;
+        int sum = 0, total;
+        for (int k = 0; k < run && from + k0 + k < to; ++k) sum += __popc(w.mask[k0 + k]);
+        int place = at + block_scan<THREADS>(sum, b.tmp, &total);
+        for (int k = 0; k < run && from + k0 + k < to; ++k) {
+            w.before[k0 + k] = place;
+            place += __popc(w.mask[k0 + k]);
+        }
+        __syncthreads();
+        each(from, to, [&](int q, int p) {
+            const unsigned m = w.mask[q - from];
+            if (!(m >> lane & 1)) return;
+            const int pos = w.before[q - from] + __popc(m & ((1u << lane) - 1));
             if (pos < c.n_pages) c.free_list[pos] = p;
             c.ref_count[p] = 0;
-        }
-        at += sum;
+        });
+        at += total;
+        __syncthreads();
     }
     cl.sync();  // remote counts are read, codes are gone
     // counts that a page listed too often left below 0
-    for (int q = q0 + wid; q < q1; q += kBkWarps) {
-        const int p = page_at(q);
+    if (b.odd) each(q0, q1, [&](int, int p) {
         if (p >= 0 && __ldcg(&c.ref_count[p]) < 0) atomicMax(&c.ref_count[p], 0);
-    }
+    });
     if (rank == 0) {
         if (threadIdx.x == 0) *c.n_free = min(all, c.n_pages);
-    }
-    cl.sync();  // every CTA has read lengths and page counts for the last time
-    if (rank == 0)
-        for (int i = threadIdx.x; i < n; i += kBkThreads)
+        for (int i = threadIdx.x; i < n; i += THREADS)
             if (b.seq[i] >= 0) c.length[b.seq[i]] = c.held[b.seq[i]] = 0;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -492,18 +554,39 @@ __global__ void __launch_bounds__(256)
     pdl_wait();
     pdl_launch();
     const int row = blockIdx.x, lane = threadIdx.x & 31;
-    // entry of the row: the number of ends at or before it
-    int e = 0;
-    for (int i = lane; i < n + lane; i += 32)
-        e += __popc(__ballot_sync(0xffffffffu, i < n && cu[i + 1] <= row));
+    // the row itself is on its way while its place is looked up
+    const int per = c.head_dim / 8, pieces = c.n_kv_heads * per;
+    const uint4 *kr = reinterpret_cast<const uint4 *>(k + row * k_stride);
+    const uint4 *vr = reinterpret_cast<const uint4 *>(v + row * v_stride);
+    uint4 head = make_uint4(0, 0, 0, 0);
+    if ((int)threadIdx.x < 2 * pieces)
+        head = (int)threadIdx.x < pieces ? kr[threadIdx.x] : vr[threadIdx.x - pieces];
+    // entry of the row: the number of ends at or before it. Lanes keep what they
+    // read of their entry, so that up to 32 entries need one round of reads.
+    int e = 0, start = 0, seq = -1;
+    for (int b = 0; b < n; b += 32) {
+        const int i = b + lane;
+        const int lo = i < n ? cu[i] : 0, hi = i < n ? cu[i + 1] : 0, q = i < n ? seqs[i] : -1;
+        const int k = __popc(__ballot_sync(0xffffffffu, i < n && hi <= row));
+        e += k;
+        if (k < 32 && e < n && e < b + 32) {
+            start = __shfl_sync(0xffffffffu, lo, k);
+            seq = __shfl_sync(0xffffffffu, q, k);
+            break;
+        }
+    }
     if (e >= n) return;  // behind the last sequence
-    const int t = row - cu[e];
-    const int s = entry_seq(c, seqs, e);
-    if (s < 0) return;
-    bool twice = false;
-    for (int i = lane; i < e + lane; i += 32)
-        twice |= __any_sync(0xffffffffu, i < e && seqs[i] == s && cu[i + 1] > cu[i]);
+    const int t = row - start, s = seq;
+    if (s < 0 || s >= c.max_seqs) {
+        if (s != -1 && threadIdx.x == 0) atomicOr(c.status, PROX_CACHE_BAD_SEQ);
+        return;
+    }
     const SeqState st = seq_state(c, s);
+    bool twice = false;
+    for (int b = 0; b < e; b += 32) {
+        const int i = b + lane;
+        twice |= __any_sync(0xffffffffu, i < e && seqs[i] == s && cu[i + 1] > cu[i]);
+    }
     const long pos = (long)st.len + t;
     if (twice || t < 0 || pos >= (long)st.held * c.page_size) {
         if (threadIdx.x == 0)
@@ -516,16 +599,14 @@ __global__ void __launch_bounds__(256)
         if (threadIdx.x == 0) atomicOr(c.status, PROX_CACHE_BAD_STATE);
         return;
     }
-    const int per = c.head_dim / 8, pieces = c.n_kv_heads * per;
     const size_t at = ((size_t)layer * c.n_pages + page) * c.n_kv_heads * c.page_size +
                       (size_t)(pos % c.page_size);
     for (int i = threadIdx.x; i < 2 * pieces; i += blockDim.x) {
         const int which = i >= pieces, p = i - which * pieces;
         const int h = p / per, d = p - h * per;
-        const uint16_t *from = which ? v + row * v_stride : k + row * k_stride;
-        uint16_t *to = which ? c.v : c.k;
-        *reinterpret_cast<uint4 *>(to + (at + (size_t)h * c.page_size) * c.head_dim + d * 8) =
-            *reinterpret_cast<const uint4 *>(from + (size_t)p * 8);
+        const uint4 x = i == (int)threadIdx.x ? head : which ? vr[p] : kr[p];
+        *reinterpret_cast<uint4 *>((which ? c.v : c.k) +
+                                   (at + (size_t)h * c.page_size) * c.head_dim + d * 8) = x;
     }
 }
 
@@ -616,12 +697,14 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     k_cache_commit(const prox_cache c, int n, const int32_t *seqs, const int32_t *path,
                    int max_path, const int32_t *n_path, uint8_t *ok_out) {
-    pdl_wait();
-    pdl_launch();
     const int i = blockIdx.x;
     SeqState st;
     int m = 0;
+    // (what is checked was there before the kernel that moves the rows let this
+    // one start, and is not changed by it)
     const int s = check_path(c, n, seqs, path, max_path, n_path, i, &st, &m, false);
+    pdl_wait();
+    pdl_launch();
     if (threadIdx.x == 0) {
         if (s >= 0 && m > 0) c.length[s] = st.len + m;
         if (ok_out) ok_out[i] = s >= 0 ? 1 : 0;
@@ -647,6 +730,52 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int block, size_t smem, cudaSt
     return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
+// clusters of more than 8 CTAs (once per device and kernel)
+cudaError_t allow_wide_cluster(const void *f) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::mutex mu;
+    static std::set<std::pair<int, const void *>> done;
+    std::lock_guard<std::mutex> lk(mu);
+    if (done.count({dev, f})) return cudaSuccess;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.insert({dev, f});
+    return e;
+}
+
+// a bookkeeping kernel on one cluster
+template <typename... P, typename... A>
+cudaError_t book(void (*kern)(P...), int ctas, int block, size_t smem, cudaStream_t s, A... args) {
+    const void *f = reinterpret_cast<const void *>(kern);
+    cudaError_t e = set_max_dynamic_smem(f, smem);
+    if (e == cudaSuccess && ctas > 8) e = allow_wide_cluster(f);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
+// the kernel's shape for n entries of cache c (see kFew)
+#define BOOK(kern, more, c, n, ...)                                                               \
+    ((n) <= kFew && (long)(n) * (c).max_pages <= kFewPages                                        \
+         ? book(kern<256, kFew>, kFewCtas, 256, sizeof(Book<kFew>) + (more), s, c, n, __VA_ARGS__) \
+     : (n) <= kSome                                                                               \
+         ? book(kern<1024, kSome>, kCtas, 1024, sizeof(Book<kSome>) + (more), s, c, n, __VA_ARGS__) \
+         : book(kern<1024, kMaxSeqs>, kCtas, 1024, sizeof(Book<kMaxSeqs>) + (more), s, c, n,      \
+                __VA_ARGS__))
+
 }  // namespace
 
 cudaError_t launch_cache_init(const prox_cache &c, cudaStream_t s) {
@@ -655,7 +784,7 @@ cudaError_t launch_cache_init(const prox_cache &c, cudaStream_t s) {
 
 cudaError_t launch_cache_reserve(const prox_cache &c, int n, const int32_t *seqs,
                                  const int32_t *n_new, uint8_t *ok, cudaStream_t s) {
-    return launch(k_cache_reserve, dim3(kCl), kBkThreads, sizeof(Book), s, c, n, seqs, n_new, ok);
+    return BOOK(k_cache_reserve, 0, c, n, seqs, n_new, ok);
 }
 
 cudaError_t launch_cache_append(const prox_cache &c, int layer, int n, const int32_t *seqs,
@@ -667,8 +796,7 @@ cudaError_t launch_cache_append(const prox_cache &c, int layer, int n, const int
 
 cudaError_t launch_cache_fork(const prox_cache &c, int n, const int32_t *src, const int32_t *dst,
                               int share, uint8_t *ok, int32_t *ws, int sms, cudaStream_t s) {
-    cudaError_t e = launch(k_cache_fork, dim3(kCl), kBkThreads, sizeof(Book), s, c, n, src, dst,
-                           share, ok, ws);
+    cudaError_t e = BOOK(k_cache_fork, 0, c, n, src, dst, share, ok, ws);
     if (e != cudaSuccess) return e;
     return launch(k_cache_copy, dim3(sms * 4), 256, 0, s, c, (const int32_t *)ws);
 }
@@ -686,7 +814,7 @@ cudaError_t launch_cache_compact(const prox_cache &c, int n, const int32_t *seqs
 }
 
 cudaError_t launch_cache_free(const prox_cache &c, int n, const int32_t *seqs, cudaStream_t s) {
-    return launch(k_cache_free, dim3(kCl), kBkThreads, sizeof(Book), s, c, n, seqs);
+    return BOOK(k_cache_free, 16 + sizeof(Window), c, n, seqs);
 }
 
 }  // namespace prox

@@ -105,7 +105,7 @@ prox_status prox_cache_reserve(const prox_cache *cache, int n, const int32_t *se
  *   k_new, v_new : device, [rows][n_kv_heads][head_dim] of the cache's type,
  *                  a row k_stride (v_stride) elements behind the one before it
  *                  (a multiple of 8, at least n_kv_heads * head_dim). Rows
- *                  from cu_new[n] on are not read.
+ *                  from cu_new[n] on have no place and are left out.
  */
 prox_status prox_cache_append(const prox_cache *cache, int layer, int n, const int32_t *seqs,
                               const int32_t *cu_new, int rows, const uint16_t *k_new,
