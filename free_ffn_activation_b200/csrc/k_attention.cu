@@ -508,14 +508,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
 
 // Joins the pieces of units that were cut. A unit is cut where a CTA's run ends
 // inside it, so the cuts are numbered by the CTAs, and a unit is joined by the
-// first cut in it. The CTAs share out steps of 32 rows and 32 columns: lanes are
+// first cut in it. The CTAs share out steps of 32 rows and CC columns: lanes are
 // rows (a piece is read in runs of 512 bytes), the pieces are dealt out to the
-// warps, whose sums meet in shared memory in a fixed order.
-template <int D, int DT>
-__global__ void __launch_bounds__(256)
+// warps, whose sums meet in shared memory in a fixed order. All reads of BATCH
+// pieces a warp are in flight at once. What has to be joined is worked out while
+// the main kernel still runs (notes that its CTAs left in the workspace instead
+// cost two more reads behind it: 11.4 against 9.8 us for one token over 1,021).
+template <int D, int DT, int CC, int BATCH>
+__global__ void __launch_bounds__(256, BATCH > 2 ? 1 : 2)
     k_attention_join(const __grid_constant__ AttnArgs a, int ROWS) {
     __shared__ Line ln;
-    __shared__ float s_o[8][32][32], s_m[8][32], s_l[8][32];
+    __shared__ float s_o[8][CC][32], s_m[8][32], s_l[8][32];
     __shared__ uint16_t s_cut[kMaxGrid];
     __shared__ int s_warp[8], s_count;
     // The line depends on the call's inputs alone, which were there before the
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(256)
     build_line(ln, a, ROWS, false);
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int G = a.n_heads / a.cache.n_kv_heads;
-    const int row_groups = (ROWS + 31) / 32, per_cut = row_groups * (D / 32);
+    const int row_groups = (ROWS + 31) / 32, per_cut = row_groups * (D / CC);
     const int run = run_length(ln, a.n, a.grid), total = ln.pre[a.n];
     // the cuts that join a unit: inside one, and the first there
     const int cuts = total ? (total - 1) / run : 0;
@@ -553,7 +556,7 @@ __global__ void __launch_bounds__(256)
         const int j = s_cut[item / per_cut], rest = item % per_cut, cut = (j + 1) * run;
         const Stretch st = stretch_at(ln, a, ROWS, cut, total);
         const int u0 = cut - st.tile0, u1 = u0 + st.all_tiles;
-        const int cc = rest % (D / 32), row0 = st.row_tile * ROWS + rest / (D / 32) * 32;
+        const int cc = rest % (D / CC), row0 = st.row_tile * ROWS + rest / (D / CC) * 32;
         const int n_rows = ln.rows[st.b] * G;
         if (row0 >= n_rows) continue;
         const int r = row0 + lane, rr = r % ROWS;  // (rows behind the last: any row's place)
@@ -562,25 +565,49 @@ __global__ void __launch_bounds__(256)
         waited = true;
         // pieces j .. c1, this warp's ones under a running maximum
         float M = -INFINITY, l = 0.f;
-        float4 o[8] = {};
-#pragma unroll 2
-        for (int c = j + wid; c <= c1; c += 8) {
-            const float *p = piece(a, c, c * run >= u0, D, ROWS);
-            const float4 *x = reinterpret_cast<const float4 *>(p) + cc * 8 * ROWS + rr;
-            float4 v[8];
+        float4 o[CC / 4] = {};
+        for (int c = j + wid; c <= c1; c += 8 * BATCH) {
+            float4 v[BATCH][CC / 4];
+            float pm[BATCH], pl[BATCH];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = __ldcg(x + k * ROWS);
-            const float pm = __ldcg(p + ROWS * D + rr), pl = __ldcg(p + ROWS * (D + 1) + rr);
-            const float nm = fmaxf(M, pm), mu = nm == -INFINITY ? 0.f : nm;
-            const float f0 = ex2(M - mu), f1 = ex2(pm - mu);
+            for (int u = 0; u < BATCH; ++u) {
+                const int k = c + 8 * u;
+                pm[u] = -INFINITY;
+                pl[u] = 0.f;
+                if (k <= c1) {
+                    const float *p = piece(a, k, k * run >= u0, D, ROWS);
+                    const float4 *x = reinterpret_cast<const float4 *>(p) + cc * (CC / 4) * ROWS + rr;
+#pragma unroll
+                    for (int y = 0; y < CC / 4; ++y) v[u][y] = __ldcg(x + y * ROWS);
+                    pm[u] = __ldcg(p + ROWS * D + rr);
+                    pl[u] = __ldcg(p + ROWS * (D + 1) + rr);
+                }
+            }
+            float nm = M;
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) nm = fmaxf(nm, pm[u]);
+            const float mu = nm == -INFINITY ? 0.f : nm, f0 = ex2(M - mu);
             M = nm;
-            l = l * f0 + pl * f1;
+            l *= f0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                o[k].x = fmaf(f1, v[k].x, o[k].x * f0);
-                o[k].y = fmaf(f1, v[k].y, o[k].y * f0);
-                o[k].z = fmaf(f1, v[k].z, o[k].z * f0);
-                o[k].w = fmaf(f1, v[k].w, o[k].w * f0);
+            for (int y = 0; y < CC / 4; ++y) {
+                o[y].x *= f0;
+                o[y].y *= f0;
+                o[y].z *= f0;
+                o[y].w *= f0;
+            }
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                if (c + 8 * u > c1) continue;
+                const float f = ex2(pm[u] - mu);
+                l = fmaf(f, pl[u], l);
+#pragma unroll
+                for (int y = 0; y < CC / 4; ++y) {
+                    o[y].x = fmaf(f, v[u][y].x, o[y].x);
+                    o[y].y = fmaf(f, v[u][y].y, o[y].y);
+                    o[y].z = fmaf(f, v[u][y].z, o[y].z);
+                    o[y].w = fmaf(f, v[u][y].w, o[y].w);
+                }
             }
         }
         const int parts = min(c1 - j + 1, 8);
@@ -589,7 +616,7 @@ __global__ void __launch_bounds__(256)
             s_m[wid][lane] = M;
             s_l[wid][lane] = l;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < CC / 4; ++k) {
                 s_o[wid][4 * k][lane] = o[k].x;
                 s_o[wid][4 * k + 1][lane] = o[k].y;
                 s_o[wid][4 * k + 2][lane] = o[k].z;
@@ -600,20 +627,23 @@ __global__ void __launch_bounds__(256)
         M = -INFINITY;
         for (int w = 0; w < parts; ++w) M = fmaxf(M, s_m[w][lane]);
         const float top = M == -INFINITY ? 0.f : M;
-        float y[4] = {};
+        constexpr int V = CC / 8;  // columns a warp
+        float y[V] = {};
         l = 0.f;
         for (int w = 0; w < parts; ++w) {
             const float f = ex2(s_m[w][lane] - top);
             l += f * s_l[w][lane];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = fmaf(f, s_o[w][wid * 4 + k][lane], y[k]);
+            for (int k = 0; k < V; ++k) y[k] = fmaf(f, s_o[w][wid * V + k][lane], y[k]);
         }
         if (r < n_rows) {
             const int t = r / G, hq = st.head * G + r - t * G;
             const size_t row = ln.row0[st.b] + t;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            *reinterpret_cast<uint2 *>(a.out + row * a.out_stride + (size_t)hq * D + cc * 32 + wid * 4) =
-                make_uint2(pack2<DT>(y[0] * inv, y[1] * inv), pack2<DT>(y[2] * inv, y[3] * inv));
+            uint32_t *op = reinterpret_cast<uint32_t *>(a.out + row * a.out_stride + (size_t)hq * D +
+                                                        cc * CC + wid * V);
+#pragma unroll
+            for (int k = 0; k < V; k += 2) op[k / 2] = pack2<DT>(y[k] * inv, y[k + 1] * inv);
             if (a.lse && cc == 0 && wid == 0)
                 a.lse[row * a.n_heads + hq] =
                     M == -INFINITY && l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
@@ -668,11 +698,14 @@ cudaError_t run_typed(const AttnArgs &a, const Plan &p, int max_rows, cudaStream
                     : p.rows == 16 ? run_main<D, DT, 1>(a, s)
                                       : run_main<D, DT, 2>(a, s);
     if (e != cudaSuccess) return e;
-    // no more CTAs than steps if every unit is cut, or than fit on the GPU at once
+    // At most so many steps of 32 rows and 16 columns, if every unit is cut. Few
+    // of them (one long sequence) want every piece's read in flight at once, many
+    // want two CTAs an SM.
     const long long units = (long long)a.n * a.cache.n_kv_heads * ((max_rows + p.rows - 1) / p.rows);
-    const long long steps = min((long long)a.grid - 1, units) * ((p.rows + 31) / 32) * (D / 32);
-    return launch(k_attention_join<D, DT>, (int)min(steps, 4LL * a.grid / p.grid_per_sm), 256, 0, s, a,
-                  p.rows);
+    const long long steps = min((long long)a.grid - 1, units) * ((p.rows + 31) / 32) * (D / 16);
+    const int sms = a.grid / p.grid_per_sm;
+    if (steps <= sms) return launch(k_attention_join<D, DT, 16, 6>, (int)steps, 256, 0, s, a, p.rows);
+    return launch(k_attention_join<D, DT, 32, 2>, (int)min(steps / 2, 4LL * sms), 256, 0, s, a, p.rows);
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
