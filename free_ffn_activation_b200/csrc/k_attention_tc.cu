@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             }
         };
         // scores of the slot's tile, into the row group's next buffer
-        auto qk = [&](int w) {
+        auto qk = [&](int w, int slot) {
             const uint32_t d = d_s + w * 128 + (n_s[w] & 1) * 64;
             const uint32_t k0 = k_lo + slot * (C::TILE >> 4);
             if (one) {
@@ -342,27 +342,27 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             pos += st.n_tiles;
             const int n_tiles = uniform(st.n_tiles);
             const bool two = NWG == 2 && uniform(ln.rows[st.b] * G - st.row_tile * ROWS > 128 ? 1 : 0);
-            // k of tile 0, then k of tile i + 1 and v of tile i
-            await();
-            wait_or_give_up(&ctl.q_ready[0], n_q[0]++, a, live);
-            tc_fence_after();
-            qk(0);
-            if (two) {
-                wait_or_give_up(&ctl.q_ready[1], n_q[1]++, a, live);
-                tc_fence_after();
-                qk(1);
-            }
-            if (one) umma_commit(&ctl.empty[slot]);
-            next();
-            for (int i = 0; i < n_tiles; ++i) {
-                if (i + 1 < n_tiles) {
-                    await();
-                    qk(0);
-                    if (two) qk(1);
-                    if (one) umma_commit(&ctl.empty[slot]);
-                    next();
-                }
+            // scores of tiles 0 and 1, then the product with v of tile i and, into
+            // the score buffer that it frees, the scores of tile i + 2
+            for (int i = 0; i < min(n_tiles, 2); ++i) {
                 await();
+#pragma unroll
+                for (int w = 0; w < NWG; ++w) {
+                    if (w == 1 && !two) continue;
+                    if (i == 0) {
+                        wait_or_give_up(&ctl.q_ready[w], n_q[w]++, a, live);
+                        tc_fence_after();
+                    }
+                    qk(w, slot);
+                }
+                if (one) umma_commit(&ctl.empty[slot]);
+                next();
+            }
+            for (int i = 0; i < n_tiles; ++i) {
+                const int sv = slot;
+                await();
+                next();
+                const bool more = i + 2 < n_tiles;
 #pragma unroll
                 for (int w = 0; w < NWG; ++w) {
                     if (w == 1 && !two) continue;
@@ -374,14 +374,21 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
 #pragma unroll
                         for (int k = 0; k < kKT / 16; ++k)
                             umma_ts(d_o + w * 128, d_s + w * 128 + buf * 64 + k * 8,
-                                    hi | (v_lo + slot * (C::TILE >> 4) + k * (2048 >> 4)), pv_idesc,
+                                    hi | (v_lo + sv * (C::TILE >> 4) + k * (2048 >> 4)), pv_idesc,
                                     k > 0 || i > 0);
                         umma_commit(&ctl.o_done[w]);
                         if (i + 1 == n_tiles) umma_commit(&ctl.o_full[w]);
+                        if (w == (two ? 1 : 0)) umma_commit(&ctl.empty[sv]);
+                    }
+                    if (more) {
+                        if (w == 0) await();
+                        qk(w, slot);
                     }
                 }
-                if (one) umma_commit(&ctl.empty[slot]);
-                next();
+                if (more) {
+                    if (one) umma_commit(&ctl.empty[slot]);
+                    next();
+                }
             }
         }
         __syncwarp();
