@@ -121,13 +121,16 @@ __device__ __forceinline__ Stretch stretch_at(const Line &ln, const AttnArgs &a,
     return s;
 }
 
-// 2-D tensor-map box global -> shared, completing on an mbarrier
+// 2-D tensor-map box global -> shared, completing on an mbarrier, with an L2
+// policy. Keys and values are evicted first: they are read once, and the cache
+// they would fill holds the kernels' instructions, the queries, the page table
+// and the pieces, whose misses each cost a microsecond of a short kernel.
 __device__ __forceinline__ void box_g2s(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                        uint64_t *bar) {
+                                        uint64_t *bar, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar)), "l"(policy)
         : "memory");
 }
 

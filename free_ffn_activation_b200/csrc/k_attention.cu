@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
         // loading warp: lane = (page of the tile, k or v, 64 elements)
         // ------------------------------------------------------------------
         constexpr int H = D / 64;
+        const uint64_t policy = l2_evict_first();
         const int pg = lane / (2 * H), kv = lane / H & 1, half = lane % H;
         bool live = true;
         int it = 0;
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
                                        : c.n_pages * c.n_kv_heads * ps;
                     box_g2s(smem_addr(sm) + slot * 2 * C::TILE + kv * C::TILE + half * C::HALF +
                                 pg * per_box * 128,
-                            kv ? &a.map_v : &a.map_k, half * 64, y, &ctl.full[slot]);
+                            kv ? &a.map_v : &a.map_k, half * 64, y, &ctl.full[slot], policy);
                 }
                 page = next;
             }

@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         // loading warp: lane = (page of the tile, 64 elements); the order of
         // slots is that of use: k0, k1, v0, k2, v1, ..., v last
         // ------------------------------------------------------------------
+        const uint64_t policy = l2_evict_first();
         const int pg = lane / H, half = lane % H;
         int it = 0;
         for (int pos = begin; pos < end && live;) {
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 __syncwarp();
                 if (wanted)
                     box_g2s(smem_addr(ring) + slot * C::TILE + half * C::HALF + pg * per_box * 128,
-                            map, half * 64, y, &ctl.full[slot]);
+                            map, half * 64, y, &ctl.full[slot], policy);
                 ++it;
             };
             int now = page_of(st.tile0), next = kNone;
