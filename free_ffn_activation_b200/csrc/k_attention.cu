@@ -507,6 +507,38 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
     }
 }
 
+// the cuts that join a unit: inside one, and the first there
+struct Cuts {
+    uint16_t at[kMaxGrid];
+    int warp[8];
+};
+__device__ int joining_cuts(const Line &ln, const AttnArgs &a, int ROWS, Cuts &c) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int run = run_length(ln, a.n, a.grid), total = ln.pre[a.n];
+    const int cuts = total ? (total - 1) / run : 0;
+    int count = 0;
+    for (int b = 0; b < cuts; b += 256) {
+        const int j = b + threadIdx.x, cut = (j + 1) * run;
+        bool joins = false;
+        if (j < cuts) {
+            const Stretch st = stretch_at(ln, a, ROWS, cut, total);
+            joins = st.tile0 > 0 && j * run <= cut - st.tile0;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, joins);
+        __syncthreads();
+        if (lane == 0) c.warp[wid] = __popc(who);
+        __syncthreads();
+        int at = count;
+        for (int w = 0; w < 8; ++w) {
+            if (w < wid) at += c.warp[w];
+            count += c.warp[w];
+        }
+        if (joins) c.at[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)j;
+    }
+    __syncthreads();
+    return count;
+}
+
 // Joins the pieces of units that were cut. A unit is cut where a CTA's run ends
 // inside it, so the cuts are numbered by the CTAs, and a unit is joined by the
 // first cut in it. The CTAs share out steps of 32 rows and CC columns: lanes are
@@ -520,8 +552,7 @@ __global__ void __launch_bounds__(256, BATCH > 2 ? 1 : 2)
     k_attention_join(const __grid_constant__ AttnArgs a, int ROWS) {
     __shared__ Line ln;
     __shared__ float s_o[8][CC][32], s_m[8][32], s_l[8][32];
-    __shared__ uint16_t s_cut[kMaxGrid];
-    __shared__ int s_warp[8], s_count;
+    __shared__ Cuts cuts;
     // The line depends on the call's inputs alone, which were there before the
     // main kernel let this one start; its pieces come after the wait.
     build_line(ln, a, ROWS, false);
@@ -529,32 +560,11 @@ __global__ void __launch_bounds__(256, BATCH > 2 ? 1 : 2)
     const int G = a.n_heads / a.cache.n_kv_heads;
     const int row_groups = (ROWS + 31) / 32, per_cut = row_groups * (D / CC);
     const int run = run_length(ln, a.n, a.grid), total = ln.pre[a.n];
-    // the cuts that join a unit: inside one, and the first there
-    const int cuts = total ? (total - 1) / run : 0;
-    if (threadIdx.x == 0) s_count = 0;
-    __syncthreads();
-    for (int b = 0; b < cuts; b += 256) {
-        const int j = b + threadIdx.x, cut = (j + 1) * run;
-        bool joins = false;
-        if (j < cuts) {
-            const Stretch st = stretch_at(ln, a, ROWS, cut, total);
-            joins = st.tile0 > 0 && j * run <= cut - st.tile0;
-        }
-        const unsigned who = __ballot_sync(0xffffffffu, joins);
-        if (lane == 0) s_warp[wid] = __popc(who);
-        __syncthreads();
-        int at = s_count;
-        for (int w = 0; w < wid; ++w) at += s_warp[w];
-        if (joins) s_cut[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)j;
-        __syncthreads();
-        if (threadIdx.x == 0)
-            for (int w = 0; w < 8; ++w) s_count += s_warp[w];
-        __syncthreads();
-    }
-    const int items = s_count * per_cut;
+    const int count = joining_cuts(ln, a, ROWS, cuts);
+    const int items = count * per_cut;
     bool waited = false;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int j = s_cut[item / per_cut], rest = item % per_cut, cut = (j + 1) * run;
+        const int j = cuts.at[item / per_cut], rest = item % per_cut, cut = (j + 1) * run;
         const Stretch st = stretch_at(ln, a, ROWS, cut, total);
         const int u0 = cut - st.tile0, u1 = u0 + st.all_tiles;
         const int cc = rest % (D / CC), row0 = st.row_tile * ROWS + rest / (D / CC) * 32;
@@ -656,6 +666,91 @@ __global__ void __launch_bounds__(256, BATCH > 2 ? 1 : 2)
     pdl_launch();
 }
 
+// The same for many units of few pieces each (a batch): a step is 32 rows with
+// all columns, a warp has 1/8 of them and goes through the pieces one after
+// another, three at a time in flight. No sums cross warps.
+template <int D, int DT>
+__global__ void __launch_bounds__(256, 3)
+    k_attention_join_few(const __grid_constant__ AttnArgs a, int ROWS) {
+    __shared__ Line ln;
+    __shared__ Cuts cuts;
+    build_line(ln, a, ROWS, false);
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int G = a.n_heads / a.cache.n_kv_heads;
+    const int row_groups = (ROWS + 31) / 32;
+    const int run = run_length(ln, a.n, a.grid), total = ln.pre[a.n];
+    const int items = joining_cuts(ln, a, ROWS, cuts) * row_groups;
+    pdl_wait();
+    pdl_launch();
+    constexpr int V = D / 32, BATCH = 3;  // float4 columns of a warp
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int j = cuts.at[item / row_groups], cut = (j + 1) * run;
+        const Stretch st = stretch_at(ln, a, ROWS, cut, total);
+        const int u0 = cut - st.tile0, c1 = (u0 + st.all_tiles - 1) / run;
+        const int row0 = st.row_tile * ROWS + item % row_groups * 32, n_rows = ln.rows[st.b] * G;
+        if (row0 >= n_rows) continue;
+        const int r = row0 + lane, rr = r % ROWS;  // (rows behind the last: any row's place)
+        float M = -INFINITY, l = 0.f;
+        float4 o[V] = {};
+        for (int c = j; c <= c1; c += BATCH) {
+            float4 v[BATCH][V];
+            float pm[BATCH], pl[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                pm[u] = -INFINITY;
+                pl[u] = 0.f;
+                if (c + u <= c1) {
+                    const float *p = piece(a, c + u, (c + u) * run >= u0, D, ROWS);
+                    const float4 *x = reinterpret_cast<const float4 *>(p) + wid * V * ROWS + rr;
+#pragma unroll
+                    for (int y = 0; y < V; ++y) v[u][y] = __ldcg(x + y * ROWS);
+                    pm[u] = __ldcg(p + ROWS * D + rr);
+                    pl[u] = __ldcg(p + ROWS * (D + 1) + rr);
+                }
+            }
+            float nm = M;
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) nm = fmaxf(nm, pm[u]);
+            const float mu = nm == -INFINITY ? 0.f : nm, f0 = ex2(M - mu);
+            M = nm;
+            l *= f0;
+#pragma unroll
+            for (int y = 0; y < V; ++y) {
+                o[y].x *= f0;
+                o[y].y *= f0;
+                o[y].z *= f0;
+                o[y].w *= f0;
+            }
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                if (c + u > c1) continue;
+                const float f = ex2(pm[u] - mu);
+                l = fmaf(f, pl[u], l);
+#pragma unroll
+                for (int y = 0; y < V; ++y) {
+                    o[y].x = fmaf(f, v[u][y].x, o[y].x);
+                    o[y].y = fmaf(f, v[u][y].y, o[y].y);
+                    o[y].z = fmaf(f, v[u][y].z, o[y].z);
+                    o[y].w = fmaf(f, v[u][y].w, o[y].w);
+                }
+            }
+        }
+        if (r >= n_rows) continue;
+        const int t = r / G, hq = st.head * G + r - t * G;
+        const size_t row = ln.row0[st.b] + t;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint4 *op = reinterpret_cast<uint4 *>(a.out + row * a.out_stride + (size_t)hq * D + wid * V * 4);
+#pragma unroll
+        for (int y = 0; y < V; y += 2)
+            op[y / 2] = make_uint4(pack2<DT>(o[y].x * inv, o[y].y * inv), pack2<DT>(o[y].z * inv, o[y].w * inv),
+                                   pack2<DT>(o[y + 1].x * inv, o[y + 1].y * inv),
+                                   pack2<DT>(o[y + 1].z * inv, o[y + 1].w * inv));
+        if (a.lse && wid == 0)
+            a.lse[row * a.n_heads + hq] =
+                M == -INFINITY && l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    }
+}
+
 template <typename... P, typename... A>
 cudaError_t launch(void (*kern)(P...), int grid, int block, size_t smem, cudaStream_t s,
                    const A &...args) {
@@ -699,14 +794,18 @@ cudaError_t run_typed(const AttnArgs &a, const Plan &p, int max_rows, cudaStream
                     : p.rows == 16 ? run_main<D, DT, 1>(a, s)
                                       : run_main<D, DT, 2>(a, s);
     if (e != cudaSuccess) return e;
-    // At most so many steps of 32 rows and 16 columns, if every unit is cut. Few
-    // of them (one long sequence) want every piece's read in flight at once, many
-    // want two CTAs an SM.
+    // One long sequence is cut into many pieces a unit, a batch into few. The
+    // former's steps want every piece's read in flight at once if the SMs have
+    // one step each at most, and two CTAs an SM otherwise.
     const long long units = (long long)a.n * a.cache.n_kv_heads * ((max_rows + p.rows - 1) / p.rows);
-    const long long steps = min((long long)a.grid - 1, units) * ((p.rows + 31) / 32) * (D / 16);
+    const long long steps = min((long long)a.grid - 1, units) * ((p.rows + 31) / 32);  // of 32 rows
     const int sms = a.grid / p.grid_per_sm;
-    if (steps <= sms) return launch(k_attention_join<D, DT, 16, 6>, (int)steps, 256, 0, s, a, p.rows);
-    return launch(k_attention_join<D, DT, 32, 2>, (int)min(steps / 2, 4LL * sms), 256, 0, s, a, p.rows);
+    if (units * 4 >= a.grid)
+        return launch(k_attention_join_few<D, DT>, (int)min(steps, 4LL * sms), 256, 0, s, a, p.rows);
+    if (steps * (D / 16) <= sms)
+        return launch(k_attention_join<D, DT, 16, 6>, (int)steps * (D / 16), 256, 0, s, a, p.rows);
+    return launch(k_attention_join<D, DT, 32, 2>, (int)min(steps * (D / 32), 4LL * sms), 256, 0, s, a,
+                  p.rows);
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,

@@ -15,8 +15,8 @@
 //            has grown by more than 2^8 since the offset in use was taken:
 //            e^(x - offset) <= 2^8 loses nothing in fp32 sums.
 //
-// One warp loads, one thread issues the MMAs, and eight warps a row group do the
-// softmax: four take the even tiles (the first score buffer), four the odd ones,
+// One warp loads, one thread a row group issues its MMAs (issuing, at some 45
+// cycles an MMA, bounds one thread), and eight warps a row group do the softmax: four take the even tiles (the first score buffer), four the odd ones,
 // so that one set forms probabilities while the other waits for scores or looks
 // for maxima. Both use one offset a row, which goes from tile to tile with a
 // token. k and v are read once for 256 rows.
@@ -46,7 +46,7 @@ struct Cfg {
     static constexpr int SLOTS =
         (ROOM - NWG * QTILE) / TILE < kMaxSlots ? (ROOM - NWG * QTILE) / TILE : kMaxSlots;
     static constexpr int SOFT = 256 * NWG;        // softmax threads
-    static constexpr int THREADS = SOFT + 64;
+    static constexpr int THREADS = SOFT + 32 * NWG + 32;
     static constexpr uint32_t COLS = NWG == 2 ? 512 : 256;  // tensor-memory columns
 };
 
@@ -60,7 +60,7 @@ struct Ctl {
     uint64_t q_ready[2], s_full[2][2], p_ready[2][2], o_done[2], o_full[2];
     uint64_t token[2][2][4];        // row group, set, warp: the row's offset is decided
     float m[2][128], l[2][2][128];  // offsets in use (log2 units); a set's sums
-    uint64_t poison[4];             // drafted tokens whose v has an infinity or NaN
+    uint64_t poison[2][4];          // drafted tokens whose v has an infinity or NaN (by stretch parity)
     uint32_t tmem;
 };
 
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&ctl.full[i], 1);
-            mbar_init(&ctl.empty[i], 1);
+            mbar_init(&ctl.empty[i], NWG);
         }
         for (int w = 0; w < NWG; ++w) {
             mbar_init(&ctl.q_ready[w], 8);
@@ -224,10 +224,11 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 for (int q = 0; q < 4; ++q) mbar_init(&ctl.token[w][b][q], 1);
             }
         }
+        for (int i = 0; i < 8; ++i) ctl.poison[i >> 2][i & 3] = 0;
         mbar_fence_init();
     }
     if (wid == 8 * NWG) tmem_alloc(&ctl.tmem, C::COLS);
-    if (wid == 8 * NWG + 1 && lane < 2)
+    if (wid == 9 * NWG && lane < 2)
         asm volatile("prefetch.tensormap [%0];" ::"l"(
                          reinterpret_cast<uint64_t>(lane ? &a.map_v : &a.map_k))
                      : "memory");
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
     const int per_box = min(ps, kKT), boxes = kKT / per_box;
     bool live = true;
 
-    if (wid == 8 * NWG + 1) {
+    if (wid == 9 * NWG) {
         // ------------------------------------------------------------------
         // loading warp: lane = (page of the tile, 64 elements); the order of
         // slots is that of use: k0, k1, v0, k2, v1, ..., v last
@@ -300,13 +301,14 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         if (!live)
             for (int k = max(0, it - SLOTS); k < it; ++k)
                 mbar_spin(&ctl.full[k % SLOTS], (k / SLOTS) & 1, 1000);
-    } else if (wid == 8 * NWG) {
+    } else if (wid >= 8 * NWG) {
         // ------------------------------------------------------------------
-        // the warp that issues the MMAs: one elected thread does, but the whole
-        // warp runs the loops on values it knows to be uniform, so that operand
-        // descriptors live in uniform registers (computed by one thread alone,
-        // an MMA took 90 cycles to issue, twice what it takes to run)
+        // a warp that issues a row group's MMAs: one elected thread does, but the
+        // whole warp runs the loops on values it knows to be uniform, so that
+        // operand descriptors live in uniform registers (computed by one thread
+        // alone, an MMA took 90 cycles to issue)
         // ------------------------------------------------------------------
+        const int w = NWG == 2 ? uniform(wid - 8 * NWG) : 0;
         constexpr uint32_t qk_idesc = idesc_of<DT>(kKT, false), pv_idesc = idesc_of<DT>(D, true);
         // low words of the descriptors of the first q, k and v tiles (the address
         // field, in 16 bytes, never carries); the high words are constants
@@ -314,10 +316,11 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                        k_lo = uniform((uint32_t)sw128_desc(smem_addr(ring), 16, 1024)),
                        v_lo = uniform((uint32_t)sw128_desc(smem_addr(ring), C::HALF, 1024));
         constexpr uint64_t hi = (uint64_t)(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
-        const uint32_t d_s = uniform(t_s), d_o = uniform(t_o);
+        const uint32_t d_s = uniform(t_s + w * 128), d_o = uniform(t_o + w * 128);
+        const uint32_t q0 = q_lo + w * (C::QTILE >> 4);
         const bool one = elect_one();
-        uint32_t n_q[2] = {}, n_s[2] = {}, n_p[2] = {};  // scores formed, probabilities used
-        int slot = 0, turn = 0;                       // of the next slot in the order of loading
+        uint32_t n_q = 0, n_s = 0, n_p = 0;  // stretches, scores formed, probabilities used
+        int slot = 0, turn = 0;              // of the next slot in the order of loading
         auto await = [&] { wait_or_give_up(&ctl.full[slot], turn, a, live); };
         auto next = [&] {
             if (++slot == SLOTS) {
@@ -325,70 +328,61 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 ++turn;
             }
         };
-        // scores of the slot's tile, into the row group's next buffer
-        auto qk = [&](int w, int slot) {
-            const uint32_t d = d_s + w * 128 + (n_s[w] & 1) * 64;
+        // scores of the slot's tile, into the next buffer
+        auto qk = [&] {
+            const uint32_t d = d_s + (n_s & 1) * 64;
             const uint32_t k0 = k_lo + slot * (C::TILE >> 4);
             if (one) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma(d, hi | (q_lo + w * (C::QTILE >> 4) + (k / 4) * (C::QHALF >> 4) + (k % 4) * 2),
+                    umma(d, hi | (q0 + (k / 4) * (C::QHALF >> 4) + (k % 4) * 2),
                          hi | (k0 + (k / 4) * (C::HALF >> 4) + (k % 4) * 2), qk_idesc, k > 0);
-                umma_commit(&ctl.s_full[w][n_s[w] & 1]);
+                umma_commit(&ctl.s_full[w][n_s & 1]);
+                umma_commit(&ctl.empty[slot]);
             }
-            ++n_s[w];
+            ++n_s;
+            next();
         };
         for (int pos = begin; pos < end;) {
             const Stretch st = stretch_at(ln, a, ROWS, pos, end);
             pos += st.n_tiles;
             const int n_tiles = uniform(st.n_tiles);
-            const bool two = NWG == 2 && uniform(ln.rows[st.b] * G - st.row_tile * ROWS > 128 ? 1 : 0);
+            if (w == 1 && uniform(ln.rows[st.b] * G - st.row_tile * ROWS) <= 128) {
+                // no rows of this group: the slots are the other one's alone
+                for (int i = 0; i < 2 * n_tiles; ++i) {
+                    await();
+                    if (one) mbar_arrive(&ctl.empty[slot]);
+                    next();
+                }
+                continue;
+            }
             // scores of tiles 0 and 1, then the product with v of tile i and, into
             // the score buffer that it frees, the scores of tile i + 2
+            wait_or_give_up(&ctl.q_ready[w], n_q++, a, live);
             for (int i = 0; i < min(n_tiles, 2); ++i) {
                 await();
-#pragma unroll
-                for (int w = 0; w < NWG; ++w) {
-                    if (w == 1 && !two) continue;
-                    if (i == 0) {
-                        wait_or_give_up(&ctl.q_ready[w], n_q[w]++, a, live);
-                        tc_fence_after();
-                    }
-                    qk(w, slot);
-                }
-                if (one) umma_commit(&ctl.empty[slot]);
-                next();
+                tc_fence_after();
+                qk();
             }
             for (int i = 0; i < n_tiles; ++i) {
-                const int sv = slot;
+                const uint32_t buf = n_p & 1, v0 = v_lo + slot * (C::TILE >> 4);
                 await();
-                next();
-                const bool more = i + 2 < n_tiles;
+                wait_or_give_up(&ctl.p_ready[w][buf], n_p >> 1, a, live);
+                ++n_p;
+                tc_fence_after();
+                if (one) {
 #pragma unroll
-                for (int w = 0; w < NWG; ++w) {
-                    if (w == 1 && !two) continue;
-                    const uint32_t buf = n_p[w] & 1;
-                    wait_or_give_up(&ctl.p_ready[w][buf], n_p[w] >> 1, a, live);
-                    ++n_p[w];
-                    tc_fence_after();
-                    if (one) {
-#pragma unroll
-                        for (int k = 0; k < kKT / 16; ++k)
-                            umma_ts(d_o + w * 128, d_s + w * 128 + buf * 64 + k * 8,
-                                    hi | (v_lo + sv * (C::TILE >> 4) + k * (2048 >> 4)), pv_idesc,
-                                    k > 0 || i > 0);
-                        umma_commit(&ctl.o_done[w]);
-                        if (i + 1 == n_tiles) umma_commit(&ctl.o_full[w]);
-                        if (w == (two ? 1 : 0)) umma_commit(&ctl.empty[sv]);
-                    }
-                    if (more) {
-                        if (w == 0) await();
-                        qk(w, slot);
-                    }
+                    for (int k = 0; k < kKT / 16; ++k)
+                        umma_ts(d_o, d_s + buf * 64 + k * 8, hi | (v0 + k * (2048 >> 4)), pv_idesc,
+                                k > 0 || i > 0);
+                    umma_commit(&ctl.empty[slot]);
+                    umma_commit(&ctl.o_done[w]);
+                    if (i + 1 == n_tiles) umma_commit(&ctl.o_full[w]);
                 }
-                if (more) {
-                    if (one) umma_commit(&ctl.empty[slot]);
-                    next();
+                next();
+                if (i + 2 < n_tiles) {
+                    await();
+                    qk();
                 }
             }
         }
@@ -402,20 +396,26 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         const uint32_t ts = t_s + w * 128 + b * 64 + lane_at, to = t_o + w * 128 + lane_at;
         const float sc = a.scale * kLog2e;
         // tiles of the row group, of this set, tokens and stretches so far
-        uint32_t n = 0, mine = 0, n_tok = 0, n_full = 0;
+        uint32_t n = 0, mine = 0, n_tok = 0, n_full = 0, odd_stretch = 0;
         int it = 0;                           // slots used by the stretches so far
+        Stretch st = {};
+        if (begin < end) st = stretch_at(ln, a, ROWS, begin, end);
         for (int pos = begin; pos < end;) {
-            const Stretch st = stretch_at(ln, a, ROWS, pos, end);
             const bool first = pos == begin;
             pos += st.n_tiles;
             const int len = ln.len[st.b], tot = ln.tot[st.b];
             const int n_rows = ln.rows[st.b] * G - st.row_tile * ROWS;  // of this row tile
             named_bar_sync(2, C::SOFT);  // all are done with the last stretch's shared values
             if (w * 128 >= n_rows) {
+                odd_stretch ^= 1;
                 it += 2 * st.n_tiles;
+                if (pos < end) st = stretch_at(ln, a, ROWS, pos, end);
                 continue;
             }
-            if (tid < 4) ctl.poison[tid] = 0;
+            // this stretch's notes; the next one's are cleared
+            uint64_t *poison = ctl.poison[odd_stretch];
+            odd_stretch ^= 1;
+            if (tid < 4) ctl.poison[odd_stretch][tid] = 0;
             const int rt = w * 128 + t;                  // row of the tile
             const bool there = rt < n_rows;
             const bool busy = rt - lane < n_rows;        // the warp has rows
@@ -424,17 +424,26 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             const size_t row = ln.row0[st.b] + tok;
             const uint64_t *tree = a.tree ? a.tree + row * a.tree_words : nullptr;
             {
-                // q: 16-byte pieces, every other one; rows behind the last one are zeros
-                const uint4 *src =
-                    reinterpret_cast<const uint4 *>(a.q + row * a.q_stride + (size_t)head * D);
-                unsigned char *dst = sq + w * C::QTILE + t * 128;
+                // q: the warp's 32 rows, half of them each set, a row's 16-byte pieces
+                // side by side (each lane knows where its own row is); rows behind the
+                // last one are zeros
+                constexpr int P = D / 8, PER = 32 / P;  // pieces of a row, rows a step
+                const int64_t mine_at = there ? (int64_t)row * a.q_stride + (int64_t)head * D : -1;
+                unsigned char *dst = sq + w * C::QTILE + (t - lane) * 128;
                 if (busy) {
+                    uint4 v[P / 2];
 #pragma unroll
-                    for (int y = 0; y < D / 16; ++y) {
-                        const int x = 2 * y + b;
-                        const uint4 v = there ? src[x] : make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(dst + (x >> 3) * C::QHALF +
-                                                   (((x & 7) ^ (t & 7)) << 4)) = v;
+                    for (int y = 0; y < P / 2; ++y) {
+                        const int k = (2 * y + b) * PER + lane / P;
+                        const int64_t from = __shfl_sync(0xffffffffu, mine_at, k);
+                        v[y] = from >= 0 ? reinterpret_cast<const uint4 *>(a.q + from)[lane % P]
+                                         : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int y = 0; y < P / 2; ++y) {
+                        const int k = (2 * y + b) * PER + lane / P, x = lane % P;
+                        *reinterpret_cast<uint4 *>(dst + k * 128 + (x >> 3) * C::QHALF +
+                                                   (((x & 7) ^ (k & 7)) << 4)) = v[y];
                     }
                 }
                 fence_proxy_async_smem();
@@ -459,40 +468,48 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 wait_or_give_up(&ctl.s_full[w][b], mine++, a, live);
                 tc_fence_after();
                 const bool edge = (tile + 1) * kKT > len;
-                if (w == 0 && edge) {
-                    // v's rows that must not meet the tensor core, one thread a
+                if (edge) {
+                    // v's rows that must not meet the tensor core, two threads a
                     // key: rows behind the last key (0 * inf is not 0), and the
                     // infinities and NaN of drafted tokens, which only some rows
-                    // see; those come back when the outputs are written
-                    const int key = tile * kKT + t;
+                    // see; those come back when the outputs are written. (Each row
+                    // group does it before its own product, to the same effect; what
+                    // was found is noted before it is taken out.)
+                    const int kr = t & (kKT - 1), key = tile * kKT + kr;
                     const int at = it + (i + 1 < st.n_tiles ? 2 * i + 2 : 2 * i + 1), slot = at % SLOTS;
                     wait_or_give_up(&ctl.full[slot], at / SLOTS, a, live);
-                    unsigned char *vr = ring + slot * C::TILE + t * 128;
-                    if (t >= kKT) {
-                    } else if (key >= tot) {
+                    // (pieces in an order that keeps a warp's rows on different banks)
+                    constexpr int P = D / 16;
+                    unsigned char *vr = ring + slot * C::TILE + kr * 128;
+                    auto piece_at = [&](int x) {
+                        const int y = (t >> 6) * P + x;
+                        return reinterpret_cast<uint4 *>(vr + (y >> 3) * C::HALF +
+                                                         (((y & 7) ^ (kr & 7)) << 4));
+                    };
+                    if (key >= tot) {
 #pragma unroll
-                        for (int x = 0; x < D / 8; ++x)
-                            *reinterpret_cast<uint4 *>(vr + (x >> 3) * C::HALF + (x & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
+                        for (int x = 0; x < P; ++x) *piece_at(x) = make_uint4(0, 0, 0, 0);
                     } else if (key >= len) {
+                        uint4 v[P];
                         bool odd = false;
-                        for (int x = 0; x < D / 8; ++x) {
-                            uint4 *p = reinterpret_cast<uint4 *>(vr + (x >> 3) * C::HALF + (x & 7) * 16);
-                            uint4 v = *p;
-                            if (non_finite2<DT>(v.x) || non_finite2<DT>(v.y) ||
-                                non_finite2<DT>(v.z) || non_finite2<DT>(v.w)) {
-                                odd = true;
-                                v.x = finite2<DT>(v.x);
-                                v.y = finite2<DT>(v.y);
-                                v.z = finite2<DT>(v.z);
-                                v.w = finite2<DT>(v.w);
-                                *p = v;
+#pragma unroll
+                        for (int x = 0; x < P; ++x) v[x] = *piece_at(x);
+#pragma unroll
+                        for (int x = 0; x < P; ++x)
+                            odd |= non_finite2<DT>(v[x].x) || non_finite2<DT>(v[x].y) ||
+                                   non_finite2<DT>(v[x].z) || non_finite2<DT>(v[x].w);
+                        if (odd) {
+                            atomicOr(reinterpret_cast<unsigned long long *>(
+                                         &poison[(key - len) >> 6 & 3]),
+                                     1ull << (key - len & 63));
+                            __threadfence_block();
+#pragma unroll 1
+                            for (int x = 0; x < P; ++x) {
+                                const uint4 u = *piece_at(x);
+                                *piece_at(x) = make_uint4(finite2<DT>(u.x), finite2<DT>(u.y),
+                                                          finite2<DT>(u.z), finite2<DT>(u.w));
                             }
                         }
-                        if (odd)
-                            atomicOr(reinterpret_cast<unsigned long long *>(
-                                         &ctl.poison[(key - len) >> 6 & 3]),
-                                     1ull << (key - len & 63));
                     }
                     fence_proxy_async_smem();
                 }
@@ -592,6 +609,8 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             // --------------------------------------------------------------
             // the rows' outputs, or a piece of them: each set half the columns
             // --------------------------------------------------------------
+            const Stretch now = st;
+            if (pos < end) st = stretch_at(ln, a, ROWS, pos, end);  // (while there is time)
             wait_or_give_up(&ctl.o_full[w], n_full++, a, live);
             tc_fence_after();
             named_bar_sync(3 + w, 256);
@@ -606,10 +625,10 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             if (busy) {
                 m = ctl.m[w][t];
                 l = ctl.l[w][0][t] + ctl.l[w][1][t];
-                const bool whole = st.n_tiles == st.all_tiles;
+                const bool whole = now.n_tiles == now.all_tiles;
                 const float inv = l == 0.f ? 0.f : whole ? 1.f / l : 1.f;
                 float *part = piece(a, blockIdx.x, first, D, ROWS);
-                const uint64_t any = ctl.poison[0] | ctl.poison[1] | ctl.poison[2] | ctl.poison[3];
+                const uint64_t any = poison[0] | poison[1] | poison[2] | poison[3];
 #pragma unroll 1
                 for (int q = b * (D / 64); q < (b + 1) * (D / 64); ++q) {
                     uint32_t ob[32];
@@ -619,17 +638,17 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                     for (int x = 0; x < 32; ++x) o[x] = __uint_as_float(ob[x]) * inv;
                     if (any && there) {
                         for (int k = 0; k < 4; ++k) {
-                            uint64_t bits = ctl.poison[k];
+                            uint64_t bits = poison[k];
                             bits &= tree ? (k < a.tree_words ? tree[k] : 0ull)
                                          : low_bits(tok + 1 - k * 64);
                             for (; bits; bits &= bits - 1) {
                                 const int key = len + k * 64 + __ffsll((long long)bits) - 1;
                                 const int page =
-                                    c.page_table[(size_t)ln.seq[st.b] * c.max_pages + (key >> sh)];
+                                    c.page_table[(size_t)ln.seq[now.b] * c.max_pages + (key >> sh)];
                                 if (!page_ok(c, page)) continue;  // (cannot be: its box was read)
                                 const uint32_t *v = reinterpret_cast<const uint32_t *>(
                                     a.v_layer +
-                                    (((size_t)page * c.n_kv_heads + st.head) * ps + (key & (ps - 1))) * D +
+                                    (((size_t)page * c.n_kv_heads + now.head) * ps + (key & (ps - 1))) * D +
                                     q * 32);
 #pragma unroll
                                 for (int x = 0; x < 32; x += 2) {
