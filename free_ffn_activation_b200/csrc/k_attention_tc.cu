@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 ++turn;
             }
         };
-        // scores of the slot's tile, into the next buffer
+        // scores of the slot's tile (there already), into the next buffer
         auto qk = [&] {
             const uint32_t d = d_s + (n_s & 1) * 64;
             const uint32_t k0 = k_lo + slot * (C::TILE >> 4);
@@ -366,7 +366,13 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             }
             for (int i = 0; i < n_tiles; ++i) {
                 const uint32_t buf = n_p & 1, v0 = v_lo + slot * (C::TILE >> 4);
+                const bool more = i + 2 < n_tiles;
+                // (a wait takes 120 cycles even when it is over: those for memory
+                // come first, so that only one lies behind the softmax)
+                uint64_t *v_free = &ctl.empty[slot];
                 await();
+                next();
+                if (more) await();
                 wait_or_give_up(&ctl.p_ready[w][buf], n_p >> 1, a, live);
                 ++n_p;
                 tc_fence_after();
@@ -375,15 +381,11 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                     for (int k = 0; k < kKT / 16; ++k)
                         umma_ts(d_o, d_s + buf * 64 + k * 8, hi | (v0 + k * (2048 >> 4)), pv_idesc,
                                 k > 0 || i > 0);
-                    umma_commit(&ctl.empty[slot]);
                     umma_commit(&ctl.o_done[w]);
                     if (i + 1 == n_tiles) umma_commit(&ctl.o_full[w]);
                 }
-                next();
-                if (i + 2 < n_tiles) {
-                    await();
-                    qk();
-                }
+                if (more) qk();
+                if (one) umma_commit(v_free);
             }
         }
         __syncwarp();
@@ -451,20 +453,24 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.q_ready[w]);
             }
-            // pages of a tile with an id out of range, one bit each (the ids of this
-            // set's next tile are on their way while one is worked on)
+            // pages with an id out of range, a bit each, of the next 32 / boxes tiles
             const int32_t *table = c.page_table + (size_t)max(ln.seq[st.b], 0) * c.max_pages;
-            auto peek = [&](int i) {
+            const int span = 32 / boxes;
+            uint32_t unreadable = 0;
+            int looked = 0;
+            auto look = [&](int i) {
                 const int key = (st.tile0 + i) * kKT + lane * per_box;
-                return i < st.n_tiles && lane < boxes && key < tot ? table[key >> sh] : 0;
+                const bool in = i + lane / boxes < st.n_tiles && key < tot;
+                unreadable = __ballot_sync(0xffffffffu, in && !page_ok(c, table[key >> sh]));
+                looked = i;
             };
             const int i0 = (n & 1) == b ? 0 : 1;  // this set's first tile
-            int page = peek(i0);
+            look(i0);
             float m = -INFINITY, l = 0.f;         // offset that l counts from, and sum
             for (int i = i0; i < st.n_tiles; i += 2) {
                 const int tile = st.tile0 + i;
-                const uint32_t bad = __ballot_sync(0xffffffffu, !page_ok(c, page));
-                page = peek(i + 2);
+                if (i - looked >= span) look(i);
+                const uint32_t bad = unreadable >> ((i - looked) * boxes) & ((1u << boxes) - 1);
                 wait_or_give_up(&ctl.s_full[w][b], mine++, a, live);
                 tc_fence_after();
                 const bool edge = (tile + 1) * kKT > len;
@@ -522,26 +528,27 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                             if (bad >> p & 1) seen &= ~(low_bits(per_box) << (p * per_box));
                         seen = there ? seen_bits(tree, a.tree_words, len, tok, tile * kKT) & seen : 0ull;
                     }
-                    // 32 scores; those not seen are -inf
-                    auto scores = [&](int q, uint32_t(&s)[32]) {
-                        tmem_get32(ts + q * 32, s);
-                        if (masked) {
-                            const uint32_t bits = (uint32_t)(seen >> q * 32);
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (!(bits >> x & 1)) s[x] = 0xff800000u;
-                        }
-                    };
-                    // (read twice: 96 registers a thread do not hold 64 of them)
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int q = 0; q < kKT / 32; ++q) {
-                        uint32_t s[32];
-                        scores(q, s);
+                    // scores not seen are -inf
+                    auto mask = [&](uint32_t bits, uint32_t(&s)[32]) {
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
-                            mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+                            if (!(bits >> x & 1)) s[x] = 0xff800000u;
+                    };
+                    // (the second half is read again for its probabilities, while the
+                    // first half's are taken: 96 registers do not hold all of it)
+                    uint32_t s0[32], s1[32];
+                    tmem_ask32(ts + 32, s1);
+                    tmem_ask32(ts, s0);
+                    tmem_take32(s1);
+                    tmem_take32(s0);
+                    if (masked) {
+                        mask((uint32_t)seen, s0);
+                        mask((uint32_t)(seen >> 32), s1);
                     }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        mx[x & 3] = fmaxf(mx[x & 3], fmaxf(__uint_as_float(s0[x]), __uint_as_float(s1[x])));
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                     // the offset that the tiles before this one left, and this one's
                     float now = -INFINITY;
@@ -582,10 +589,8 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                     const float mu = m == -INFINITY ? 0.f : m;
                     const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                    for (int q = 0; q < kKT / 32; ++q) {
-                        uint32_t s[32], p[16];
-                        scores(q, s);
+                    auto probabilities = [&](const uint32_t(&s)[32], uint32_t at) {
+                        uint32_t p[16];
 #pragma unroll
                         for (int x = 0; x < 32; x += 2) {
                             const float2 z = fma2(
@@ -594,8 +599,13 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                             sum[x / 2 & 1] = add2(sum[x / 2 & 1], e);
                             p[x / 2] = pack2<DT>(e.x, e.y);
                         }
-                        tmem_st16(ts + q * 16, p);
-                    }
+                        tmem_st16(at, p);
+                    };
+                    tmem_ask32(ts + 32, s1);
+                    probabilities(s0, ts);
+                    tmem_take32(s1);
+                    if (masked) mask((uint32_t)(seen >> 32), s1);
+                    probabilities(s1, ts + 16);
                     sum[0] = add2(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
                     tmem_st_wait();
