@@ -15,11 +15,11 @@
 //            has grown by more than 2^8 since the offset in use was taken:
 //            e^(x - offset) <= 2^8 loses nothing in fp32 sums.
 //
-// One warp loads, one thread a row group issues its MMAs (issuing, at some 45
-// cycles an MMA, bounds one thread), and eight warps a row group do the softmax: four take the even tiles (the first score buffer), four the odd ones,
-// so that one set forms probabilities while the other waits for scores or looks
-// for maxima. Both use one offset a row, which goes from tile to tile with a
-// token. k and v are read once for 256 rows.
+// One warp loads, one thread a row group issues its MMAs, and four warps a row
+// group do the softmax, a row a thread with up to 168 registers: a tile's scores
+// stay in registers from the maximum to the probabilities, half of the next
+// tile's are fetched meanwhile, and their product runs one tile ahead. k and v
+// are read once for 256 rows.
 #include "attention.cuh"
 #include "umma.cuh"
 
@@ -45,7 +45,7 @@ struct Cfg {
     static constexpr int ROOM = (NWG == 2 ? 210 : 102) * 1024;
     static constexpr int SLOTS =
         (ROOM - NWG * QTILE) / TILE < kMaxSlots ? (ROOM - NWG * QTILE) / TILE : kMaxSlots;
-    static constexpr int SOFT = 256 * NWG;        // softmax threads
+    static constexpr int SOFT = 128 * NWG;        // softmax threads
     static constexpr int THREADS = SOFT + 32 * NWG + 32;
     static constexpr uint32_t COLS = NWG == 2 ? 512 : 256;  // tensor-memory columns
 };
@@ -58,8 +58,6 @@ struct Ctl {
     // per row group: q written; scores there and probabilities there (two
     // buffers); a tile's second product done, and that of a stretch's last tile
     uint64_t q_ready[2], s_full[2][2], p_ready[2][2], o_done[2], o_full[2];
-    uint64_t token[2][2][4];        // row group, set, warp: the row's offset is decided
-    float m[2][128], l[2][2][128];  // offsets in use (log2 units); a set's sums
     uint64_t poison[2][4];          // drafted tokens whose v has an infinity or NaN (by stretch parity)
     uint32_t tmem;
 };
@@ -215,20 +213,19 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             mbar_init(&ctl.empty[i], NWG);
         }
         for (int w = 0; w < NWG; ++w) {
-            mbar_init(&ctl.q_ready[w], 8);
+            mbar_init(&ctl.q_ready[w], 4);
             mbar_init(&ctl.o_done[w], 1);
             mbar_init(&ctl.o_full[w], 1);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&ctl.s_full[w][b], 1);
                 mbar_init(&ctl.p_ready[w][b], 4);
-                for (int q = 0; q < 4; ++q) mbar_init(&ctl.token[w][b][q], 1);
             }
         }
         for (int i = 0; i < 8; ++i) ctl.poison[i >> 2][i & 3] = 0;
         mbar_fence_init();
     }
-    if (wid == 8 * NWG) tmem_alloc(&ctl.tmem, C::COLS);
-    if (wid == 9 * NWG && lane < 2)
+    if (wid == 4 * NWG) tmem_alloc(&ctl.tmem, C::COLS);
+    if (wid == 5 * NWG && lane < 2)
         asm volatile("prefetch.tensormap [%0];" ::"l"(
                          reinterpret_cast<uint64_t>(lane ? &a.map_v : &a.map_k))
                      : "memory");
@@ -245,7 +242,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
     const int per_box = min(ps, kKT), boxes = kKT / per_box;
     bool live = true;
 
-    if (wid == 9 * NWG) {
+    if (wid == 5 * NWG) {
         // ------------------------------------------------------------------
         // loading warp: lane = (page of the tile, 64 elements); the order of
         // slots is that of use: k0, k1, v0, k2, v1, ..., v last
@@ -301,14 +298,14 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         if (!live)
             for (int k = max(0, it - SLOTS); k < it; ++k)
                 mbar_spin(&ctl.full[k % SLOTS], (k / SLOTS) & 1, 1000);
-    } else if (wid >= 8 * NWG) {
+    } else if (wid >= 4 * NWG) {
         // ------------------------------------------------------------------
         // a warp that issues a row group's MMAs: one elected thread does, but the
         // whole warp runs the loops on values it knows to be uniform, so that
         // operand descriptors live in uniform registers (computed by one thread
         // alone, an MMA took 90 cycles to issue)
         // ------------------------------------------------------------------
-        const int w = NWG == 2 ? uniform(wid - 8 * NWG) : 0;
+        const int w = NWG == 2 ? uniform(wid - 4 * NWG) : 0;
         constexpr uint32_t qk_idesc = idesc_of<DT>(kKT, false), pv_idesc = idesc_of<DT>(D, true);
         // low words of the descriptors of the first q, k and v tiles (the address
         // field, in 16 bytes, never carries); the high words are constants
@@ -391,15 +388,15 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         __syncwarp();
     } else {
         // ------------------------------------------------------------------
-        // softmax: set b of row group w, one thread a row
+        // softmax: row group w, one thread a row
         // ------------------------------------------------------------------
-        const int w = wid >> 3, b = wid >> 2 & 1, t = tid & 127;
+        const int w = wid >> 2, t = tid & 127;
         const uint32_t lane_at = (uint32_t)(wid & 3) << 21;   // first tensor-memory lane << 16
-        const uint32_t ts = t_s + w * 128 + b * 64 + lane_at, to = t_o + w * 128 + lane_at;
+        const uint32_t to = t_o + w * 128 + lane_at;
         const float sc = a.scale * kLog2e;
-        // tiles of the row group, of this set, tokens and stretches so far
-        uint32_t n = 0, mine = 0, n_tok = 0, n_full = 0, odd_stretch = 0;
-        int it = 0;                           // slots used by the stretches so far
+        // tiles and stretches of the row group so far, slots used by all stretches
+        uint32_t n = 0, n_full = 0, odd_stretch = 0;
+        int it = 0;
         Stretch st = {};
         if (begin < end) st = stretch_at(ln, a, ROWS, begin, end);
         for (int pos = begin; pos < end;) {
@@ -407,7 +404,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             pos += st.n_tiles;
             const int len = ln.len[st.b], tot = ln.tot[st.b];
             const int n_rows = ln.rows[st.b] * G - st.row_tile * ROWS;  // of this row tile
-            named_bar_sync(2, C::SOFT);  // all are done with the last stretch's shared values
+            named_bar_sync(2, C::SOFT);  // all are done with the notes of the last stretch
             if (w * 128 >= n_rows) {
                 odd_stretch ^= 1;
                 it += 2 * st.n_tiles;
@@ -426,24 +423,22 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             const size_t row = ln.row0[st.b] + tok;
             const uint64_t *tree = a.tree ? a.tree + row * a.tree_words : nullptr;
             {
-                // q: the warp's 32 rows, half of them each set, a row's 16-byte pieces
-                // side by side (each lane knows where its own row is); rows behind the
-                // last one are zeros
+                // q: the warp's 32 rows, a row's 16-byte pieces side by side (each lane
+                // knows where its own row is); rows behind the last one are zeros
                 constexpr int P = D / 8, PER = 32 / P;  // pieces of a row, rows a step
                 const int64_t mine_at = there ? (int64_t)row * a.q_stride + (int64_t)head * D : -1;
                 unsigned char *dst = sq + w * C::QTILE + (t - lane) * 128;
                 if (busy) {
-                    uint4 v[P / 2];
+                    uint4 v[P];
 #pragma unroll
-                    for (int y = 0; y < P / 2; ++y) {
-                        const int k = (2 * y + b) * PER + lane / P;
-                        const int64_t from = __shfl_sync(0xffffffffu, mine_at, k);
+                    for (int y = 0; y < P; ++y) {
+                        const int64_t from = __shfl_sync(0xffffffffu, mine_at, y * PER + lane / P);
                         v[y] = from >= 0 ? reinterpret_cast<const uint4 *>(a.q + from)[lane % P]
                                          : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int y = 0; y < P / 2; ++y) {
-                        const int k = (2 * y + b) * PER + lane / P, x = lane % P;
+                    for (int y = 0; y < P; ++y) {
+                        const int k = y * PER + lane / P, x = lane % P;
                         *reinterpret_cast<uint4 *>(dst + k * 128 + (x >> 3) * C::QHALF +
                                                    (((x & 7) ^ (k & 7)) << 4)) = v[y];
                     }
@@ -464,15 +459,27 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 unreadable = __ballot_sync(0xffffffffu, in && !page_ok(c, table[key >> sh]));
                 looked = i;
             };
-            const int i0 = (n & 1) == b ? 0 : 1;  // this set's first tile
-            look(i0);
-            float m = -INFINITY, l = 0.f;         // offset that l counts from, and sum
-            for (int i = i0; i < st.n_tiles; i += 2) {
+            look(0);
+            float m = -INFINITY, l = 0.f;         // offset in use (log2 units) and sum
+            uint32_t s0[32], s1[32];              // scores
+            // tile i's buffer; its scores are there after the wait
+            auto buffer = [&](int i) { return t_s + w * 128 + ((n + i) & 1) * 64 + lane_at; };
+            auto formed = [&](int i) {
+                wait_or_give_up(&ctl.s_full[w][(n + i) & 1], (n + i) >> 1, a, live);
+                tc_fence_after();
+            };
+            formed(0);
+            if (busy) tmem_ask32(buffer(0), s0);
+            for (int i = 0; i < st.n_tiles; ++i) {
                 const int tile = st.tile0 + i;
+                const uint32_t ts = buffer(i);
+                if (busy) {
+                    tmem_ask32(ts + 32, s1);
+                    tmem_take32(s0);
+                    tmem_take32(s1);
+                }
                 if (i - looked >= span) look(i);
                 const uint32_t bad = unreadable >> ((i - looked) * boxes) & ((1u << boxes) - 1);
-                wait_or_give_up(&ctl.s_full[w][b], mine++, a, live);
-                tc_fence_after();
                 const bool edge = (tile + 1) * kKT > len;
                 if (edge) {
                     // v's rows that must not meet the tensor core, two threads a
@@ -534,13 +541,6 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                         for (int x = 0; x < 32; ++x)
                             if (!(bits >> x & 1)) s[x] = 0xff800000u;
                     };
-                    // (the second half is read again for its probabilities, while the
-                    // first half's are taken: 96 registers do not hold all of it)
-                    uint32_t s0[32], s1[32];
-                    tmem_ask32(ts + 32, s1);
-                    tmem_ask32(ts, s0);
-                    tmem_take32(s1);
-                    tmem_take32(s0);
                     if (masked) {
                         mask((uint32_t)seen, s0);
                         mask((uint32_t)(seen >> 32), s1);
@@ -550,16 +550,11 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                     for (int x = 0; x < 32; ++x)
                         mx[x & 3] = fmaxf(mx[x & 3], fmaxf(__uint_as_float(s0[x]), __uint_as_float(s1[x])));
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                    // the offset that the tiles before this one left, and this one's
-                    float now = -INFINITY;
-                    if (i > 0) {
-                        wait_or_give_up(&ctl.token[w][b][wid & 3], n_tok++, a, live);
-                        now = ctl.m[w][t];
-                    }
-                    if (__any_sync(0xffffffffu, top > now + kGrow || (top > now && now == -INFINITY))) {
-                        const float nm = fmaxf(now, top);
-                        const float f = nm > now ? ex2(now - nm) : 1.f;
-                        now = nm;
+                    if (__any_sync(0xffffffffu, top > m + kGrow || (top > m && m == -INFINITY))) {
+                        const float nm = fmaxf(m, top);
+                        const float f = nm > m ? ex2(m - nm) : 1.f;
+                        m = nm;
+                        l *= f;
                         if (i > 0) {
                             // Products up to the last tile's are in the outputs then. (A
                             // wait tells a phase by its parity: tile i's scores were
@@ -579,13 +574,6 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                             }
                         }
                     }
-                    ctl.m[w][t] = now;
-                    __syncwarp();
-                    if (lane == 0 && i + 1 < st.n_tiles) mbar_arrive(&ctl.token[w][b ^ 1][wid & 3]);
-                    if (now > m) {
-                        l *= ex2(m - now);
-                        m = now;
-                    }
                     const float mu = m == -INFINITY ? 0.f : m;
                     const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -601,46 +589,39 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                         }
                         tmem_st16(at, p);
                     };
-                    tmem_ask32(ts + 32, s1);
                     probabilities(s0, ts);
-                    tmem_take32(s1);
-                    if (masked) mask((uint32_t)(seen >> 32), s1);
+                    if (i + 1 < st.n_tiles) {
+                        formed(i + 1);
+                        tmem_ask32(buffer(i + 1), s0);
+                    }
                     probabilities(s1, ts + 16);
                     sum[0] = add2(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
                     tmem_st_wait();
                 }
+                else if (i + 1 < st.n_tiles) {
+                    formed(i + 1);
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_ready[w][b]);
+                if (lane == 0) mbar_arrive(&ctl.p_ready[w][(n + i) & 1]);
             }
             it += 2 * st.n_tiles;
             n += st.n_tiles;
             // --------------------------------------------------------------
-            // the rows' outputs, or a piece of them: each set half the columns
+            // the rows' outputs, or a piece of them
             // --------------------------------------------------------------
             const Stretch now = st;
             if (pos < end) st = stretch_at(ln, a, ROWS, pos, end);  // (while there is time)
             wait_or_give_up(&ctl.o_full[w], n_full++, a, live);
             tc_fence_after();
-            named_bar_sync(3 + w, 256);
             if (busy) {
-                // the last offset is the one of the last tile's set; the other set's
-                // sum counts from what it last saw
-                const float last = ctl.m[w][t];
-                ctl.l[w][b][t] = m == -INFINITY ? 0.f : l * ex2(m - last);
-                __syncwarp();
-            }
-            named_bar_sync(3 + w, 256);
-            if (busy) {
-                m = ctl.m[w][t];
-                l = ctl.l[w][0][t] + ctl.l[w][1][t];
                 const bool whole = now.n_tiles == now.all_tiles;
                 const float inv = l == 0.f ? 0.f : whole ? 1.f / l : 1.f;
                 float *part = piece(a, blockIdx.x, first, D, ROWS);
                 const uint64_t any = poison[0] | poison[1] | poison[2] | poison[3];
 #pragma unroll 1
-                for (int q = b * (D / 64); q < (b + 1) * (D / 64); ++q) {
+                for (int q = 0; q < D / 32; ++q) {
                     uint32_t ob[32];
                     tmem_get32(to + q * 32, ob);
                     float o[32];
@@ -686,10 +667,10 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                                                    pack2<DT>(o[x + 6], o[x + 7]));
                     }
                 }
-                if (b == 0 && !whole) {
+                if (!whole) {
                     part[ROWS * D + rt] = m;
                     part[ROWS * (D + 1) + rt] = l;
-                } else if (b == 0 && there && a.lse) {
+                } else if (there && a.lse) {
                     a.lse[row * a.n_heads + head] =
                         m == -INFINITY && l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
@@ -698,7 +679,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         }
     }
     __syncthreads();
-    if (wid == 8 * NWG) tmem_free(tmem, C::COLS);
+    if (wid == 4 * NWG) tmem_free(tmem, C::COLS);
 }
 
 template <int D, int DT, int NWG>
