@@ -149,6 +149,30 @@ struct Elem<PROX_FP16> {
     }
 };
 
+// a maximum and the sums that go with it
+struct Part {
+    float m;
+    double s0, s1;
+};
+// the parts of the warp's first N lanes as one, in a fixed order (in lane 0)
+template <int N>
+__device__ __forceinline__ Part join_parts(Part p) {
+    float M = p.m;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float z = max_nan((p.m - M) * kLog2e, -1e30f);
+    const double r = (double)ex2(z);
+    p.s1 = r * (p.s1 + (double)z * p.s0);
+    p.s0 = r * p.s0;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+        p.s0 += __shfl_xor_sync(0xffffffffu, p.s0, o);
+        p.s1 += __shfl_xor_sync(0xffffffffu, p.s1, o);
+    }
+    p.m = M;
+    return p;
+}
+
 struct Shared {
     alignas(16) unsigned long long cand[kCand + 8];  // key << 32 | ~index
     alignas(16) unsigned long long joined[kMaxSplit * kMaxTop + 8];  // all CTAs' (first CTA)
@@ -156,8 +180,7 @@ struct Shared {
     unsigned long long sorted[kMaxTop];
     float m[kWarps];
     double s0[kWarps], s1[kWarps];
-    float cta_m;                                     // the CTA's sums, read by the first one
-    double cta_s0, cta_s1;
+    Part cta;                                        // the CTA's sums, read by the first one
     uint32_t warp_key[kWarps];
     int n_cand, n_best;
     int lost;                                        // candidates did not fit
@@ -427,20 +450,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a, i
         }
     }
     __syncthreads();
-    if (tid == 0) {
-        float M = sh.m[0];
-        for (int w = 1; w < kWarps; ++w) M = max_nan(M, sh.m[w]);
-        double t0 = 0, t1 = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            const float z = max_nan((sh.m[w] - M) * kLog2e, -1e30f);
-            const double r = (double)ex2(z);
-            t0 += r * sh.s0[w];
-            t1 += r * (sh.s1[w] + (double)z * sh.s0[w]);
+    if (wid == 0) {
+        const Part p = join_parts<kWarps>({lane < kWarps ? sh.m[lane] : -FLT_MAX,
+                                           lane < kWarps ? sh.s0[lane] : 0.0,
+                                           lane < kWarps ? sh.s1[lane] : 0.0});
+        if (lane == 0) {
+            sh.cta = p;
+            if (TOP) sh.n_best = sh.n_cand;
         }
-        sh.cta_m = M;
-        sh.cta_s0 = t0;
-        sh.cta_s1 = t1;
-        if (TOP) sh.n_best = sh.n_cand;
     }
     if (split > 1) {
         cl.sync();
@@ -451,34 +468,29 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a, i
     } else {
         __syncthreads();
     }
-    if (tid == 0) {
-        float M = sh.cta_m;
-        for (int r = 1; r < split; ++r) M = max_nan(M, *cl.map_shared_rank(&sh.cta_m, r));
-        double t0 = 0, t1 = 0;
-        for (int r = 0; r < split; ++r) {
-            const Shared *o = r ? cl.map_shared_rank(&sh, r) : &sh;
-            const float z = max_nan((o->cta_m - M) * kLog2e, -1e30f);
-            const double w = (double)ex2(z);
-            t0 += w * o->cta_s0;
-            t1 += w * (o->cta_s1 + (double)z * o->cta_s0);
+    if (TOP && split > 1) {
+        // places without a code are 0 and come last
+        const int r = tid / k, i = tid - r * k;
+        if (r < split) {
+            const Shared *o = cl.map_shared_rank(&sh, r);
+            sh.joined[tid] = i < o->n_best ? o->best[i] : 0;
         }
-        const double ls = log(t0);
-        sh.lse_m = M;
-        sh.log_s0 = ls;
-        if (a.entropy)
-            a.entropy[row] = t0 == 0 ? 0.f : (float)(ls - 0.6931471805599453 * (t1 / t0));
     }
-    int found = 0;
-    if constexpr (TOP) {
-        if (split > 1) {
-            for (int r = 0; r < split; ++r) {
-                const Shared *o = r ? cl.map_shared_rank(&sh, r) : &sh;
-                const int c = o->n_best;
-                if (tid < c) sh.joined[found + tid] = o->best[tid];
-                found += c;
-            }
-            select_top(sh.joined, found, k, sh.sorted);
+    if (wid == 0) {
+        Part p = {-FLT_MAX, 0.0, 0.0};
+        if (lane < split) p = cl.map_shared_rank(&sh, lane)->cta;
+        p = join_parts<kMaxSplit>(p);
+        if (lane == 0) {
+            const double ls = log(p.s0);
+            sh.lse_m = p.m;
+            sh.log_s0 = ls;
+            if (a.entropy)
+                a.entropy[row] = p.s0 == 0 ? 0.f : (float)(ls - 0.6931471805599453 * (p.s1 / p.s0));
         }
+    }
+    if (TOP && split > 1) {
+        __syncthreads();
+        select_top(sh.joined, split * k, k, sh.sorted);
     }
     __syncthreads();
     const float M = sh.lse_m;
