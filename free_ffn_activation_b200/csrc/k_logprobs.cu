@@ -250,6 +250,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a, i
     const int v0 = first + min(rank * per, nvec), v1 = first + min((rank + 1) * per, nvec);
     const int k = a.top_k;
 
+    // the given tokens' logits are on their way meanwhile (one a thread; more
+    // than that are read at the end)
+    float given = __uint_as_float(0x7fc00000u);
+    if (rank == 0 && tid < a.n_tok) {
+        const int t = a.tokens[row * a.n_tok + tid];
+        if (t >= 0 && t < a.vocab) given = E::load(base, t);
+    }
+
     // a finite start, so that z is never inf - inf where nothing was seen yet
     float m = -FLT_MAX, s0 = 0.f, s1 = 0.f;
     // makes vm's maximum the running one (s1 in units of log2)
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a, i
     float flv = key_value(0);  // NaN: nothing is below it
     int steps = 0, refresh = 1;
     fetch(v0 + tid);
-#pragma unroll 2
+#pragma unroll(TOP && N == 8 ? 1 : 2)
     for (int vb = v0; vb < v1; vb += kStep) {
         const int v = vb + tid;
         uint4 cur[kUnroll];
@@ -506,7 +514,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a, i
             a.top_logp[row * k + tid] = logp(key_value((uint32_t)(code >> 32)));
         }
     }
-    for (int i = tid; i < a.n_tok; i += kThreads) {
+    // (NaN for a token out of range goes through)
+    if (tid < a.n_tok) a.logp[row * a.n_tok + tid] = isnan(given) ? given : logp(given);
+    for (int i = tid + kThreads; i < a.n_tok; i += kThreads) {
         const int t = a.tokens[row * a.n_tok + i];
         a.logp[row * a.n_tok + i] =
             t >= 0 && t < a.vocab ? logp(E::load(base, t)) : __uint_as_float(0x7fc00000u);
