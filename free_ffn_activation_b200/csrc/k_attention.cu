@@ -775,15 +775,21 @@ cudaError_t run_main(const AttnArgs &a, cudaStream_t s) {
     return launch(k_attention<D, DT, RG>, a.grid, kThreads, smem, s, a);
 }
 
-// How a call runs: row tiles of 16 or 32 rows on mma.sync, of 128 or 256 rows on
-// the tensor memory's MMA
+// How a call runs, by the rows of a key/value head (drafted tokens x heads that
+// share it) and the number of heads over all sequences: row tiles of 16 or 32 rows
+// on mma.sync, of 128 or 256 rows on the tensor memory's MMA. Measured (us, head
+// dim 128, 8 key/value heads of 4 heads, 64-token pages; mma.sync | tcgen05):
+//                            4 rows      16 rows     32 rows     48 rows
+//   1 sequence of 1,021     9.6 | 14.0   9.6 | 15.6  10.3 | 16.1   - | 16.5
+//   1 sequence of 16,383   20.7 | 27.1  23.4 | 30.3  26.4 | 31.3   - | 32.1
+//   24 sequences of 3,000  58.5 | 62.9  59.7 | 64.4  75.9 | 65.6   - | 69.2
 struct Plan {
     int rows, grid_per_sm;
     bool tc;
 };
-Plan plan_of(int max_rows) {
+Plan plan_of(int max_rows, long long heads, int sms) {
     if (max_rows <= 16) return {16, 2, false};
-    if (max_rows <= 32) return {32, 2, false};
+    if (max_rows <= 32 && heads * 2 < sms) return {32, 2, false};
     if (max_rows <= 128) return {128, 2, true};
     return {256, 1, true};
 }
@@ -845,25 +851,26 @@ bool encode_rows(CUtensorMap *map, const prox_cache &c, const uint16_t *base) {
 
 }  // namespace
 
-// tiles that one sequence can have at most
+// tiles that one sequence can have at most, in the smallest row tiles
 static long long tiles_of_one(const prox_cache &c, int max_rows) {
-    const Plan p = plan_of(max_rows);
-    return (long long)c.n_kv_heads * ((max_rows + p.rows - 1) / p.rows) *
+    const int rows = max_rows <= 128 ? 128 : 256;  // (fewer rows are one tile of any kind)
+    return (long long)c.n_kv_heads * ((max_rows + rows - 1) / rows) *
            ((long long)c.max_pages * c.page_size / kKT + 1);
 }
 
 bool attention_fits(const prox_cache &c, int max_rows) { return tiles_of_one(c, max_rows) < 1ll << 31; }
 
 size_t attention_part_bytes(int head_dim, int max_rows, int sms) {
-    const Plan p = plan_of(max_rows);
-    return (size_t)sms * p.grid_per_sm * 2 * piece_floats(head_dim, p.rows) * sizeof(float);
+    // (for any number of heads: many take the larger row tile)
+    const Plan p = plan_of(max_rows, 1 << 30, sms);
+    const size_t grid = min(sms * p.grid_per_sm, kMaxGrid);
+    return grid * 2 * piece_floats(head_dim, p.rows) * sizeof(float);
 }
 
 cudaError_t launch_attention(AttnArgs &a, const uint16_t *k_layer, int max_rows, int sms,
                              cudaStream_t s) {
-    const Plan p = plan_of(max_rows);
-    if (!encode_rows(&a.map_k, a.cache, k_layer) ||
-        !encode_rows(&a.map_v, a.cache, a.v_layer))
+    const Plan p = plan_of(max_rows, (long long)min(a.n, kGroup) * a.cache.n_kv_heads, sms);
+    if (!encode_rows(&a.map_k, a.cache, k_layer) || !encode_rows(&a.map_v, a.cache, a.v_layer))
         return cudaErrorInvalidValue;
     a.grid = min(sms * p.grid_per_sm, kMaxGrid);
     const int32_t *seqs = a.seqs, *cu = a.cu_q;
