@@ -15,8 +15,6 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 #include <mutex>
-#include <set>
-#include <utility>
 
 namespace cg = cooperative_groups;
 
@@ -730,18 +728,33 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int block, size_t smem, cudaSt
     return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
-// clusters of more than 8 CTAs (once per device and kernel)
-cudaError_t allow_wide_cluster(const void *f) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
+// whether the device has a place for the kernel's cluster of more than 8 CTAs,
+// which needs as many free SMs side by side (asked once per device and kernel)
+bool wide_cluster_fits(const void *f, const cudaLaunchConfig_t &cfg) {
+    struct Known {
+        const void *f;
+        int dev;
+        bool fits;
+    };
+    static Known known[256];
+    static int n_known = 0;
     static std::mutex mu;
-    static std::set<std::pair<int, const void *>> done;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
     std::lock_guard<std::mutex> lk(mu);
-    if (done.count({dev, f})) return cudaSuccess;
-    e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) done.insert({dev, f});
-    return e;
+    int at = 0;
+    while (at < n_known && (known[at].f != f || known[at].dev != dev)) ++at;
+    bool fits;
+    if (at < n_known) {
+        fits = known[at].fits;
+    } else {
+        int clusters = 0;
+        fits = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+               cudaOccupancyMaxActiveClusters(&clusters, f, &cfg) == cudaSuccess && clusters > 0;
+        if (!fits) cudaGetLastError();
+        if (n_known < 256) known[n_known++] = {f, dev, fits};
+    }
+    return fits;
 }
 
 // a bookkeeping kernel on one cluster
@@ -749,7 +762,6 @@ template <typename... P, typename... A>
 cudaError_t book(void (*kern)(P...), int ctas, int block, size_t smem, cudaStream_t s, A... args) {
     const void *f = reinterpret_cast<const void *>(kern);
     cudaError_t e = set_max_dynamic_smem(f, smem);
-    if (e == cudaSuccess && ctas > 8) e = allow_wide_cluster(f);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
@@ -764,6 +776,10 @@ cudaError_t book(void (*kern)(P...), int ctas, int block, size_t smem, cudaStrea
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    if (ctas > 8 && !wide_cluster_fits(f, cfg)) {
+        cfg.gridDim = dim3(8);
+        attr[1].val.clusterDim.x = 8;
+    }
     return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 

@@ -197,6 +197,61 @@ def test_many_sequences_and_pages(gpu):
     assert b.m.n_free == [9000]
 
 
+@pytest.mark.parametrize("n", [33, 255, 257, 700, 1024, 1025])
+def test_entries_around_the_sizes_of_a_call(gpu, n):
+    """Every call with n entries, some padding and some without tokens."""
+    b = Both(*make(gpu, layers=1, pages=6 * n, kv_heads=1, seqs=2 * n + 2, cols=3, page=16, dim=64))
+    rng = random.Random(n)
+    seqs = list(range(n))
+    rng.shuffle(seqs)
+    for i in rng.sample(range(n), 3):
+        seqs[i] = -1
+    counts = [rng.randint(0, 5) for _ in seqs]
+    b.reserve(seqs, counts)
+    b.append(seqs, counts, extra=2)
+    b.check()
+    b.compact(seqs, [[0, 2, 4]] * n, [min(1, c) if c < 5 else 3 for c in counts])
+    b.check()
+    dst = [n + i for i in range(n)]
+    b.fork(seqs, dst, share=False)
+    b.check()
+    b.free(dst)
+    b.fork(seqs, dst)
+    b.check()
+    b.free(seqs)
+    b.check()
+    b.free(dst)
+    b.check()
+    assert b.m.n_free == [6 * n]
+
+
+def test_freeing_more_listings_than_a_block_keeps(gpu):
+    """4000 forks of a sequence of 2048 pages, a quarter with a page of their own."""
+    n, cols, pages = 4000, 2050, 4000
+    c = D.PagedCache(1, pages, 1, 16, 64, n + 1, cols, torch.bfloat16, gpu)
+    D.cache_reserve(c, ints([n], gpu), ints([2048 * 16], gpu))
+    c.length[n] = 2048 * 16
+    seqs = torch.arange(n, dtype=torch.int32, device=gpu)
+    D.cache_fork(c, torch.full_like(seqs, n), seqs)
+    some = seqs[::4].contiguous()
+    D.cache_reserve(c, some, torch.ones_like(some))
+    torch.cuda.synchronize()
+    assert D.cache_status(c) == (P.PROX_OK, 0)
+    table, held = c.page_table.cpu(), c.held.cpu()
+    assert held.tolist() == [2048 + (s % 4 == 0) for s in range(n)] + [2048]
+    assert int(c.ref_count.max()) == n + 1
+    left = int(c.n_free)
+    assert left == pages - 2048 - 1000
+    order = torch.cat([seqs.flip(0).cpu(), torch.tensor([n], dtype=torch.int32)])
+    listed = torch.cat([table[s, :held[s]] for s in order.tolist()]).tolist()
+    want = c.free_list[:left].tolist() + list(dict.fromkeys(listed))
+    D.cache_free(c, order.to(gpu))
+    torch.cuda.synchronize()
+    assert D.cache_status(c) == (P.PROX_OK, 0)
+    assert int(c.n_free) == pages and c.free_list.tolist() == want
+    assert int(c.ref_count.abs().max()) == 0 and int(c.held.max()) == 0 and int(c.length.max()) == 0
+
+
 def test_corrupt_state_is_reported_and_stays_in_bounds(gpu):
     c, _ = make(gpu)
     D.cache_reserve(c, ints([0, 1], gpu), ints([40, 40], gpu))
