@@ -168,7 +168,8 @@ PROX_API prox_status prox_tree_attention(const prox_cache *cache, int layer, int
         (long long)rows * n_heads > 1ll << 31)
         return PROX_EINVAL;
     const int max_rows = max_q * (n_heads / cache->n_kv_heads);
-    if (!std::isfinite(scale) || !(scale > 0.f)) return PROX_EINVAL;
+    // (scores are kept in units of log 2, so the factor times log2(e) is used)
+    if (!(scale > 0.f) || !std::isfinite(scale * 1.44269504f)) return PROX_EINVAL;
     if (tree && (tree_words < (max_q + 63) / 64 || tree_words > 1 << 20)) return PROX_EINVAL;
     if (n == 0 || rows == 0) return PROX_OK;
     if (!have(seqs, 4) || !have(cu_q, 4) || !have(q) || !aligned(tree, 8) || !have(out) || !aligned(lse, 4) ||
@@ -199,7 +200,7 @@ PROX_API prox_status prox_tree_attention(const prox_cache *cache, int layer, int
     a.out_stride = out_stride;
     a.lse = lse;
     a.part = static_cast<float *>(ws);
-    a.wait_us = kDefaultWaitUs;
+    attention_test_state(&a.wait_us, &a.debug_skip);
     return done(launch_attention(a, cache->k + layer * one, max_rows, sms, (cudaStream_t)stream));
 }
 

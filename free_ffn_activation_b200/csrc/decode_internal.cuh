@@ -45,7 +45,10 @@ struct AttnArgs {
     float *part;                            // partial results, see k_attention.cu
     int grid;                               // CTAs of the main kernel
     uint32_t wait_us;                       // wall-clock bound of each wait, microseconds
+    int debug_skip;                         // test hook: CTA 0 never loads this slot (-1: off)
 };
+// the bound of the waits and, from the test hook, the slot not to load (-1: none)
+void attention_test_state(uint32_t *wait_us, int *skip);
 // whether a sequence's tiles can be numbered in 31 bits
 bool attention_fits(const prox_cache &c, int max_rows);
 size_t attention_part_bytes(int head_dim, int max_rows, int sms);
@@ -92,9 +95,11 @@ __device__ __forceinline__ bool page_ok(const prox_cache &c, int p) {
 }
 
 // Bounded wait on the phase of `bar` with the given parity, for handovers of a
-// microsecond: tries without a sleep hint, and looks at the clock only now and
-// then. False once limit_us microseconds have passed.
-__device__ __forceinline__ bool mbar_spin(uint64_t *bar, uint32_t parity, uint32_t limit_us) {
+// microsecond: tries without a sleep hint, and looks at the clock and at `dead`
+// (if there is one: a wait elsewhere in the CTA has given up) only now and then.
+// False once limit_us microseconds have passed, or *dead is set.
+__device__ __forceinline__ bool mbar_spin(uint64_t *bar, uint32_t parity, uint32_t limit_us,
+                                          const volatile uint32_t *dead = nullptr) {
     const uint32_t addr = smem_addr(bar);
     uint64_t t0 = 0;
     for (uint32_t tries = 0;; ++tries) {
@@ -110,7 +115,7 @@ __device__ __forceinline__ bool mbar_spin(uint64_t *bar, uint32_t parity, uint32
         if ((tries & 63u) == 63u) {
             const uint64_t now = global_ns();
             if (!t0) t0 = now;
-            if (now - t0 > (uint64_t)limit_us * 1000u) return false;
+            if ((dead && *dead) || now - t0 > (uint64_t)limit_us * 1000u) return false;
         }
     }
 }

@@ -16,9 +16,10 @@
 //
 // In a CTA one warp loads: tensor-map boxes of one page's rows and 64 elements,
 // 128-byte swizzled, into a ring of stages on mbarriers. Four warps compute
-// with mma.sync m16n8k16 (bf16 or fp16, fp32 sums): up to 64 rows the tensor
-// pipes keep up with the memory, and a warp's registers carry a tile of
-// scores straight into the second product.
+// with mma.sync m16n8k16 (bf16 or fp16, fp32 sums) on tiles of 16 or 32 rows:
+// with so few rows the tensor pipes keep up with the memory, and a warp's
+// registers carry a tile of scores straight into the second product. More
+// rows take the kernel of k_attention_tc.cu; plan_of has the rule.
 #include "attention.cuh"
 
 #include <cuda_runtime.h>
@@ -80,6 +81,7 @@ static_assert(sizeof(Line) % 16 == 0, "barriers are 8-byte aligned");
 struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t poison;              // drafted keys of the tile whose v is not finite
+    uint32_t dead;                // a wait has given up
     uint32_t bad[kMaxStages];     // pages of the stage's tile with an id out of range
     float m[kWarps * 16], l[kWarps * 16];
 };
@@ -124,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
             mbar_init(&ctl.empty[i], kWarps);
         }
         ctl.poison = 0;
+        ctl.dead = 0;
         mbar_fence_init();
     }
     pdl_wait();
@@ -157,9 +160,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
             for (int i = 0; i < st.n_tiles; ++i, ++it) {
                 const int tile = st.tile0 + i, slot = it % NST;
                 const int next = i + 1 < st.n_tiles ? page_of(tile + 1) : kNone;
-                if (!__all_sync(0xffffffffu, it < NST || mbar_spin(&ctl.empty[slot],
-                                                                   (it / NST - 1) & 1, a.wait_us))) {
+                if (!__all_sync(0xffffffffu, it < NST || mbar_spin(&ctl.empty[slot], (it / NST - 1) & 1,
+                                                                   a.wait_us, &ctl.dead))) {
                     live = false;
+                    ctl.dead = 1;
                     if (lane == 0) atomicOr(c.status, PROX_CACHE_TIMEOUT);
                     break;
                 }
@@ -167,7 +171,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
                 const bool wanted = page != kNone, good = page >= 0 && page < c.n_pages;
                 const unsigned bad = __ballot_sync(0xffffffffu, wanted && !good);
                 const unsigned load = __ballot_sync(0xffffffffu, wanted);
-                if (lane == 0) {
+                const bool skip = blockIdx.x == 0 && it == a.debug_skip;
+                if (lane == 0 && !skip) {
                     uint32_t pages = 0;
                     for (int p = 0; p < boxes; ++p) pages |= (bad >> (p * 2 * H) & 1u) << p;
                     if (pages) atomicOr(c.status, PROX_CACHE_BAD_STATE);
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
                     mbar_arrive_expect_tx(&ctl.full[slot], __popc(load) * per_box * 128);
                 }
                 __syncwarp();
-                if (wanted) {
+                if (wanted && !skip) {
                     const int y = good ? (page * c.n_kv_heads + st.head) * ps + tile * kKT % ps
                                        : c.n_pages * c.n_kv_heads * ps;
                     box_g2s(smem_addr(sm) + slot * 2 * C::TILE + kv * C::TILE + half * C::HALF +
@@ -186,10 +191,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
             }
             if (!live) break;
         }
-        // after a wait that gave up: let the copies in flight land
-        if (!live)
-            for (int k = max(0, it - NST); k < it; ++k)
-                mbar_spin(&ctl.full[k % NST], (k / NST) & 1, 1000);
+        // no copy is in flight when the CTA ends, not behind a wait that gave up either
+        for (int k = max(0, it - NST); k < it; ++k)
+            mbar_spin(&ctl.full[k % NST], (k / NST) & 1, a.wait_us);
         return;
     }
 
@@ -234,8 +238,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
 
         for (int i = 0; i < st.n_tiles; ++i, ++it) {
             const int tile = st.tile0 + i, slot = it % NST;
-            if (live && !mbar_spin(&ctl.full[slot], (it / NST) & 1, a.wait_us)) {
+            if (live && !mbar_spin(&ctl.full[slot], (it / NST) & 1, a.wait_us, &ctl.dead)) {
                 live = false;
+                ctl.dead = 1;
                 if (lane == 0) atomicOr(c.status, PROX_CACHE_TIMEOUT);
             }
             __syncwarp();  // (lanes may have seen the phase end at different tries)
@@ -402,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.empty[slot]);
+            // (a slot that was not waited for may be under way: it is not given back)
+            if (lane == 0 && live) mbar_arrive(&ctl.empty[slot]);
         }
 
         // ------------------------------------------------------------------

@@ -59,7 +59,8 @@ struct Ctl {
     // buffers); a tile's second product done, and that of a stretch's last tile
     uint64_t q_ready[2], s_full[2][2], p_ready[2][2], o_done[2], o_full[2];
     uint64_t poison[2][4];          // drafted tokens whose v has an infinity or NaN (by stretch parity)
-    uint32_t tmem;
+    uint64_t drained[2];            // behind a wait that gave up: a row group's MMAs are done
+    uint32_t tmem, dead;            // a wait has given up
 };
 
 template <int D, int NWG>
@@ -184,9 +185,10 @@ __device__ __forceinline__ T uniform(T x) {
 // all. Lanes may see the phase end at different tries, and what follows (named
 // barriers, tensor-memory loads) wants the warp together again.
 __device__ __forceinline__ void wait_or_give_up(uint64_t *bar, uint32_t count, const AttnArgs &a,
-                                                bool &live) {
-    if (live && !mbar_spin(bar, count & 1, a.wait_us)) {
+                                                Ctl &ctl, bool &live) {
+    if (live && !mbar_spin(bar, count & 1, a.wait_us, &ctl.dead)) {
         live = false;
+        ctl.dead = 1;
         atomicOr(a.cache.status, PROX_CACHE_TIMEOUT);
     }
     __syncwarp();
@@ -216,11 +218,13 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             mbar_init(&ctl.q_ready[w], 4);
             mbar_init(&ctl.o_done[w], 1);
             mbar_init(&ctl.o_full[w], 1);
+            mbar_init(&ctl.drained[w], 1);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&ctl.s_full[w][b], 1);
                 mbar_init(&ctl.p_ready[w][b], 4);
             }
         }
+        ctl.dead = 0;
         for (int i = 0; i < 8; ++i) ctl.poison[i >> 2][i & 3] = 0;
         mbar_fence_init();
     }
@@ -262,9 +266,10 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             // one tile of k or v into the next slot
             auto load = [&](const CUtensorMap *map, int tile, int page) {
                 const int slot = it % SLOTS;
-                if (!__all_sync(0xffffffffu, it < SLOTS || mbar_spin(&ctl.empty[slot],
-                                                                     (it / SLOTS - 1) & 1, a.wait_us))) {
+                if (!__all_sync(0xffffffffu, it < SLOTS || mbar_spin(&ctl.empty[slot], (it / SLOTS - 1) & 1,
+                                                                     a.wait_us, &ctl.dead))) {
                     live = false;
+                    ctl.dead = 1;
                     if (lane == 0) atomicOr(c.status, PROX_CACHE_TIMEOUT);
                     return;
                 }
@@ -274,10 +279,11 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 const int y = good ? (page * c.n_kv_heads + st.head) * ps + (tile * kKT & (ps - 1))
                                    : c.n_pages * c.n_kv_heads * ps;
                 if (wanted && !good) atomicOr(c.status, PROX_CACHE_BAD_STATE);
-                if (lane == 0)
+                const bool skip = blockIdx.x == 0 && it == a.debug_skip;
+                if (lane == 0 && !skip)
                     mbar_arrive_expect_tx(&ctl.full[slot], __popc(load) * per_box * 128);
                 __syncwarp();
-                if (wanted)
+                if (wanted && !skip)
                     box_g2s(smem_addr(ring) + slot * C::TILE + half * C::HALF + pg * per_box * 128,
                             map, half * 64, y, &ctl.full[slot], policy);
                 ++it;
@@ -294,16 +300,16 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 now = next;
             }
         }
-        // after a wait that gave up: let the copies in flight land
-        if (!live)
-            for (int k = max(0, it - SLOTS); k < it; ++k)
-                mbar_spin(&ctl.full[k % SLOTS], (k / SLOTS) & 1, 1000);
+        // no copy is in flight when the CTA ends, not behind a wait that gave up either
+        for (int k = max(0, it - SLOTS); k < it; ++k)
+            mbar_spin(&ctl.full[k % SLOTS], (k / SLOTS) & 1, a.wait_us);
     } else if (wid >= 4 * NWG) {
         // ------------------------------------------------------------------
         // a warp that issues a row group's MMAs: one elected thread does, but the
         // whole warp runs the loops on values it knows to be uniform, so that
         // operand descriptors live in uniform registers (computed by one thread
-        // alone, an MMA took 90 cycles to issue)
+        // alone, an MMA took 90 cycles to issue); after a wait that gave up nothing
+        // more is issued
         // ------------------------------------------------------------------
         const int w = NWG == 2 ? uniform(wid - 4 * NWG) : 0;
         constexpr uint32_t qk_idesc = idesc_of<DT>(kKT, false), pv_idesc = idesc_of<DT>(D, true);
@@ -318,7 +324,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         const bool one = elect_one();
         uint32_t n_q = 0, n_s = 0, n_p = 0;  // stretches, scores formed, probabilities used
         int slot = 0, turn = 0;              // of the next slot in the order of loading
-        auto await = [&] { wait_or_give_up(&ctl.full[slot], turn, a, live); };
+        auto await = [&] { wait_or_give_up(&ctl.full[slot], turn, a, ctl, live); };
         auto next = [&] {
             if (++slot == SLOTS) {
                 slot = 0;
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         auto qk = [&] {
             const uint32_t d = d_s + (n_s & 1) * 64;
             const uint32_t k0 = k_lo + slot * (C::TILE >> 4);
-            if (one) {
+            if (one && live) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     umma(d, hi | (q0 + (k / 4) * (C::QHALF >> 4) + (k % 4) * 2),
@@ -348,14 +354,14 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 // no rows of this group: the slots are the other one's alone
                 for (int i = 0; i < 2 * n_tiles; ++i) {
                     await();
-                    if (one) mbar_arrive(&ctl.empty[slot]);
+                    if (one && live) mbar_arrive(&ctl.empty[slot]);
                     next();
                 }
                 continue;
             }
             // scores of tiles 0 and 1, then the product with v of tile i and, into
             // the score buffer that it frees, the scores of tile i + 2
-            wait_or_give_up(&ctl.q_ready[w], n_q++, a, live);
+            wait_or_give_up(&ctl.q_ready[w], n_q++, a, ctl, live);
             for (int i = 0; i < min(n_tiles, 2); ++i) {
                 await();
                 tc_fence_after();
@@ -370,10 +376,10 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 await();
                 next();
                 if (more) await();
-                wait_or_give_up(&ctl.p_ready[w][buf], n_p >> 1, a, live);
+                wait_or_give_up(&ctl.p_ready[w][buf], n_p >> 1, a, ctl, live);
                 ++n_p;
                 tc_fence_after();
-                if (one) {
+                if (one && live) {
 #pragma unroll
                     for (int k = 0; k < kKT / 16; ++k)
                         umma_ts(d_o, d_s + buf * 64 + k * 8, hi | (v0 + k * (2048 >> 4)), pv_idesc,
@@ -382,8 +388,13 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                     if (i + 1 == n_tiles) umma_commit(&ctl.o_full[w]);
                 }
                 if (more) qk();
-                if (one) umma_commit(v_free);
+                if (one && live) umma_commit(v_free);
             }
+        }
+        if (one && !live) {
+            // the MMAs issued come to their end before the tensor memory is freed
+            umma_commit(&ctl.drained[w]);
+            mbar_spin(&ctl.drained[w], 0, kDefaultWaitUs);
         }
         __syncwarp();
     } else {
@@ -465,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             // tile i's buffer; its scores are there after the wait
             auto buffer = [&](int i) { return t_s + w * 128 + ((n + i) & 1) * 64 + lane_at; };
             auto formed = [&](int i) {
-                wait_or_give_up(&ctl.s_full[w][(n + i) & 1], (n + i) >> 1, a, live);
+                wait_or_give_up(&ctl.s_full[w][(n + i) & 1], (n + i) >> 1, a, ctl, live);
                 tc_fence_after();
             };
             formed(0);
@@ -490,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                     // was found is noted before it is taken out.)
                     const int kr = t & (kKT - 1), key = tile * kKT + kr;
                     const int at = it + (i + 1 < st.n_tiles ? 2 * i + 2 : 2 * i + 1), slot = at % SLOTS;
-                    wait_or_give_up(&ctl.full[slot], at / SLOTS, a, live);
+                    wait_or_give_up(&ctl.full[slot], at / SLOTS, a, ctl, live);
                     // (pieces in an order that keeps a warp's rows on different banks)
                     constexpr int P = D / 16;
                     unsigned char *vr = ring + slot * C::TILE + kr * 128;
@@ -561,7 +572,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                             // formed behind the product of tile i - 2, and tile i's own
                             // product waits for this thread, so it is the phase of tile
                             // i - 1 or the one behind it that is under way.)
-                            wait_or_give_up(&ctl.o_done[w], n + i - 1, a, live);
+                            wait_or_give_up(&ctl.o_done[w], n + i - 1, a, ctl, live);
                             tc_fence_after();
 #pragma unroll 1
                             for (int q = 0; q < D / 16; ++q) {
@@ -613,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             // --------------------------------------------------------------
             const Stretch now = st;
             if (pos < end) st = stretch_at(ln, a, ROWS, pos, end);  // (while there is time)
-            wait_or_give_up(&ctl.o_full[w], n_full++, a, live);
+            wait_or_give_up(&ctl.o_full[w], n_full++, a, ctl, live);
             tc_fence_after();
             if (busy) {
                 const bool whole = now.n_tiles == now.all_tiles;

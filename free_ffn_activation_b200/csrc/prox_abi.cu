@@ -207,7 +207,12 @@ static uint32_t g_spin_limit = kDefaultWaitUs;
 static int g_debug_skip = -1;
 // prox_test_set_skip: which kernel's arrival CTA 0 skips (kSkip*) and where
 static int g_skip_where = 0, g_skip_pos = -1;
-constexpr int kSkipStage1Tc = 1, kSkipStage2Tc = 3;
+constexpr int kSkipStage1Tc = 1, kSkipStage2Tc = 3, kSkipAttention = 4;
+void attention_test_state(uint32_t *wait_us, int *skip);  // decode_internal.cuh
+void attention_test_state(uint32_t *wait_us, int *skip) {
+    *wait_us = g_spin_limit;
+    *skip = g_skip_where == kSkipAttention ? g_skip_pos : -1;
+}
 // measurement hook (prox_test_set_stamps): phase stamps of the next passes
 static unsigned long long *g_stamps = nullptr;
 

@@ -174,7 +174,7 @@ prox_status prox_cache_status(const prox_cache *cache, void *stream, uint32_t *f
  *          max_q rows (1 <= max_q <= 256).
  *   tree : device, uint64 [rows][tree_words] or NULL; tree_words >=
  *          ceil(max_q / 64). Bits d >= T are ignored.
- *   scale: finite and > 0.
+ *   scale: > 0, and scale * log2(e) finite in fp32.
  *   out  : device, the cache's type, [rows][n_heads][head_dim], rows
  *          out_stride elements apart (as q_stride).
  *   lse  : device, fp32 [rows][n_heads], or NULL.

@@ -46,6 +46,8 @@ void prox_test_set_stamps(unsigned long long *slots);
  *      the MMA thread never signals group `position` done (status bit 5);
  *   3  the tensor-core Stage 2: the up/gate loaders never complete their
  *      step `position` (status bit 5);
+ *   4  tree attention: the loading warp of CTA 0 never fills its slot
+ *      `position` (PROX_CACHE_TIMEOUT in the cache's status word);
  *   0  off.
  * Nothing faults: the kernel records the timeout in the status word, skips
  * the rest of its MMAs, waits (with the default bound) for those already

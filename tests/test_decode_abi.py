@@ -114,6 +114,11 @@ def test_attention_arguments(over):
     assert attend(fake(), **over) == P.PROX_EINVAL
 
 
+def test_scales_whose_log2_form_overflows():
+    assert attend(fake(), scale=2.4e38) == P.PROX_EINVAL
+    assert attend(fake(), scale=2.3e38, n=0) == P.PROX_OK
+
+
 def test_attention_of_nothing_is_ok():
     assert attend(fake(), n=0, seqs=None, q=None, out=None, ws=None) == P.PROX_OK
     assert attend(fake(), rows=0, seqs=None, q=None, out=None, ws=None) == P.PROX_OK

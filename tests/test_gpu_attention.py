@@ -258,6 +258,44 @@ def test_two_streams_with_a_workspace_each(gpu):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
 
 
+# rows of a head for the kernels of 16 and 32 rows, of 128 and of 256 rows
+@pytest.mark.parametrize("group,draft,position", [(4, 4, 0), (4, 4, 1), (2, 12, 2), (4, 20, 0), (4, 20, 1),
+                                                  (4, 20, 4), (8, 40, 0), (8, 40, 3), (8, 40, 6)])
+def test_a_load_that_never_comes_is_reported(gpu, group, draft, position):
+    """The waits run out, the call ends with an error, and the next one is right."""
+    c = Drafted(gpu, [30000, 600], [draft, draft], group=group, page=32, tree="random")
+    P.test_set_wait(20000)
+    P.test_set_skip(P.SKIP_ATTENTION, position)
+    try:
+        c.run()
+    finally:
+        P.test_set_skip(P.SKIP_OFF)
+        P.test_set_wait(0)
+    assert D.cache_status(c.cache) == (P.PROX_ETIMEOUT, D.CACHE_TIMEOUT)
+    c.check(*c.run())
+    assert D.cache_status(c.cache) == (P.PROX_OK, 0)
+
+
+# the tensor-memory kernel: one and two groups of 128 rows, a last tile of few rows
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("group,draft", [(5, 8), (5, 28), (8, 37)])
+def test_many_rows_of_types_dims_pages(gpu, dim, dtype, page, group, draft):
+    c = Drafted(gpu, [130, 0, 7, 700], [draft, draft - 1, 1, draft // 2], dim=dim, dtype=dtype, page=page,
+                group=group, tree="random", order=[3, 0, 1, 2], seed=page)
+    c.check(*c.run())
+    assert D.cache_status(c.cache) == (P.PROX_OK, 0)
+
+
+@pytest.mark.parametrize("group,draft", [(4, 24), (4, 64), (8, 40)])
+def test_runs_over_many_long_units(gpu, group, draft):
+    """A block's run holds the end of one unit, whole ones, and the start of another."""
+    for lens in ([9001] * 3, [4100, 9, 12000, 64, 700, 2500]):
+        c = Drafted(gpu, lens, [draft] * len(lens), group=group, kv_heads=8, page=64, tree="random", seed=draft)
+        c.check(*c.run())
+
+
 @pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two devices")
 def test_another_device_than_the_current_one():
     c = Drafted(torch.device("cuda:1"), [200], [3])
