@@ -89,14 +89,15 @@ def _ints(t: torch.Tensor, shape: tuple, dev: torch.device, name: str, dtype=tor
 
 def _rows(t: torch.Tensor, heads: int, dim: int, dtype, dev: torch.device, name: str) -> tuple:
     """(pointer, row stride) of [rows][heads][dim] whose rows are contiguous."""
-    if t.dtype is not dtype or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or \
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 3 or shape[1] != heads or shape[2] != dim or \
             t.device != dev:
         raise ValueError(f"{name} must be a {dtype} tensor [rows][{heads}][{dim}] on {dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != dim):
+    if s[2] != 1 or (s[1] != dim and heads > 1):
         raise ValueError(f"{name}: a row's heads must be contiguous, got strides {s}")
-    return t.data_ptr(), s[0] if t.shape[0] > 1 else heads * dim
+    return t.data_ptr(), s[0] if shape[0] > 1 else heads * dim
 
 
 # ---------------------------------------------------------------------------
@@ -254,27 +255,35 @@ def tree_attention(cache: PagedCache, layer: int, q: torch.Tensor, seqs: torch.T
     the cache. tree int64 [rows][words] has the bits of the drafted tokens each
     row sees; None is a chain. scale defaults to head_dim ** -0.5. Rows behind
     the last sequence are left as they are in out and lse."""
-    dev = cache.device
-    n, heads = seqs.numel(), q.shape[1] if q.dim() == 3 else 0
-    qp, qs = _rows(q, heads, cache.head_dim, cache.dtype, dev, "q")
-    rows = q.shape[0]
+    # (outputs made here are not checked, and made from sizes given one by one: the
+    # shortest calls take less time on the GPU than on the host)
+    dev, dim = cache.device, cache.head_dim
+    n, shape = seqs.numel(), q.shape
+    heads = shape[1] if len(shape) == 3 else 0
+    qp, qs = _rows(q, heads, dim, cache.dtype, dev, "q")
+    rows = shape[0]
     if out is None:
-        out = q.new_empty((rows, heads, cache.head_dim))
-    elif out.shape != q.shape:
-        raise ValueError(f"out must have shape {tuple(q.shape)}, got {tuple(out.shape)}")
-    op, os_ = _rows(out, heads, cache.head_dim, cache.dtype, dev, "out")
+        out = torch.empty(rows, heads, dim, dtype=cache.dtype, device=dev)
+        op, os_ = out.data_ptr(), heads * dim
+    elif out.shape != shape:
+        raise ValueError(f"out must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    else:
+        op, os_ = _rows(out, heads, dim, cache.dtype, dev, "out")
     if lse is None:
-        lse = q.new_empty((rows, heads), dtype=torch.float32)
+        lse = torch.empty(rows, heads, dtype=torch.float32, device=dev)
+        lp = lse.data_ptr()
+    else:
+        lp = _ints(lse, (rows, heads), dev, "lse", torch.float32)
     if ws is None:
         ws = attention_workspace(cache, max_q, heads)
+    size = ws.numel()
     words = 0
     if tree is not None:
         words = tree.shape[1] if tree.dim() == 2 else -1
         tree = _ints(tree, (rows, words), dev, "tree", torch.int64)
     a = (layer, n, _ints(seqs, (n,), dev, "seqs"), _ints(cu_q, (n + 1,), dev, "cu_q"), rows, max_q,
-         heads, qp, qs, tree, words, cache.head_dim ** -0.5 if scale is None else float(scale), op,
-         os_, _ints(lse, (rows, heads), dev, "lse", torch.float32),
-         _ints(ws, (ws.numel(),), dev, "ws", torch.uint8), ws.numel())
+         heads, qp, qs, tree, words, dim ** -0.5 if scale is None else float(scale), op, os_, lp,
+         _ints(ws, (size,), dev, "ws", torch.uint8), size)
     with _on(dev):
         P._check(_lib().prox_tree_attention(cache._ref, *a, _stream(dev)), "prox_tree_attention")
     return out, lse
@@ -311,10 +320,10 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, *,
         n_tok = tokens.shape[1] if tokens.dim() == 2 else -1
         tp = _ints(tokens, (rows, n_tok), dev, "tokens")
     f32, k = torch.float32, top_k > 0
-    out = LogprobsOut(logits.new_empty((rows, n_tok), dtype=f32) if n_tok else None,
-                      logits.new_empty((rows,), dtype=f32),
-                      logits.new_empty((rows, top_k), dtype=torch.int32) if k else None,
-                      logits.new_empty((rows, top_k), dtype=f32) if k else None)
+    out = LogprobsOut(torch.empty(rows, n_tok, dtype=f32, device=dev) if n_tok else None,
+                      torch.empty(rows, dtype=f32, device=dev),
+                      torch.empty(rows, top_k, dtype=torch.int32, device=dev) if k else None,
+                      torch.empty(rows, top_k, dtype=f32, device=dev) if k else None)
     a = (rows, vocab, DTYPES[logits.dtype], logits.data_ptr(),
          logits.stride(0) if rows > 1 else vocab, tp if n_tok else None, n_tok, top_k,
          P._ptr(out.logp), out.entropy.data_ptr(), P._ptr(out.top_ids), P._ptr(out.top_logp))
