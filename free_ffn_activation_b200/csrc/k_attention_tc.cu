@@ -181,6 +181,21 @@ __device__ __forceinline__ T uniform(T x) {
     return __shfl_sync(0xffffffffu, x, 0);
 }
 
+// The queries into L2, a few lines a thread, by all CTAs together: where each
+// CTA's rows are is known only after the line, and its reads would then stand
+// behind the first stages of keys and values of all CTAs (64 drafted tokens of 32
+// heads over 32,749 tokens: 62.1 -> 61.5 us).
+__device__ __forceinline__ void prefetch_queries(const AttnArgs &a, int D) {
+    const unsigned per_row = a.n_heads * (D / 64);  // lines of 128 bytes
+    const unsigned step = gridDim.x * blockDim.x;
+    const unsigned lines = (unsigned)min((long long)a.rows * per_row, 4ll * step);
+    for (unsigned i = ((threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 + (threadIdx.x & 31); i < lines;
+         i += step) {
+        const unsigned row = i / per_row;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + row * a.q_stride + (i - row * per_row) * 64));
+    }
+}
+
 // bounded wait of a whole warp; once one has given up, later ones do not wait at
 // all. Lanes may see the phase end at different tries, and what follows (named
 // barriers, tensor-memory loads) wants the warp together again.
@@ -235,6 +250,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                      : "memory");
     pdl_wait();
     pdl_launch();
+    prefetch_queries(a, D);
     tc_fence_before();
     build_line(ln, a, ROWS, blockIdx.x == 0);  // (its barriers cover the setup above)
     tc_fence_after();
@@ -410,10 +426,34 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         int it = 0;
         Stretch st = {};
         if (begin < end) st = stretch_at(ln, a, ROWS, begin, end);
+        // A row of a stretch's tile: its drafted token and head, whether it exists. Worked
+        // out anew where it is wanted (q, masks, outputs): kept over the loop of tiles, it
+        // took registers that the scores then had to leave for local memory (16 sequences
+        // of 8,000 to 32,000 tokens: 427 -> 401 us). With one row group there is room for
+        // the token alone, which spares short units a division (ragged batch 41.9 -> 40.3).
+        struct Place {
+            int tok, head;
+            size_t row;
+            const uint64_t *tree;
+            bool there;
+        };
+        auto token = [&](const Stretch &s, int rt) {
+            const int r = s.row_tile * ROWS + rt;
+            return r < ln.rows[s.b] * G ? r / G : 0;
+        };
+        auto place = [&](const Stretch &s, int rt, int tok) {
+            Place p;
+            const int r = s.row_tile * ROWS + rt;
+            p.there = r < ln.rows[s.b] * G;
+            p.tok = tok;
+            p.head = s.head * G + (p.there ? r - p.tok * G : 0);
+            p.row = (size_t)ln.row0[s.b] + p.tok;
+            p.tree = a.tree ? a.tree + p.row * a.tree_words : nullptr;
+            return p;
+        };
         for (int pos = begin; pos < end;) {
             const bool first = pos == begin;
             pos += st.n_tiles;
-            const int len = ln.len[st.b], tot = ln.tot[st.b];
             const int n_rows = ln.rows[st.b] * G - st.row_tile * ROWS;  // of this row tile
             named_bar_sync(2, C::SOFT);  // all are done with the notes of the last stretch
             if (w * 128 >= n_rows) {
@@ -423,21 +463,19 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 continue;
             }
             // this stretch's notes; the next one's are cleared
-            uint64_t *poison = ctl.poison[odd_stretch];
             odd_stretch ^= 1;
             if (tid < 4) ctl.poison[odd_stretch][tid] = 0;
+            auto poison = [&]() -> uint64_t * { return ctl.poison[odd_stretch ^ 1]; };
             const int rt = w * 128 + t;                  // row of the tile
-            const bool there = rt < n_rows;
+            const int tok = token(st, rt);
             const bool busy = rt - lane < n_rows;        // the warp has rows
-            const int r = st.row_tile * ROWS + rt;
-            const int tok = there ? r / G : 0, head = st.head * G + (there ? r - tok * G : 0);
-            const size_t row = ln.row0[st.b] + tok;
-            const uint64_t *tree = a.tree ? a.tree + row * a.tree_words : nullptr;
             {
+                const Place me = place(st, rt, tok);
                 // q: the warp's 32 rows, a row's 16-byte pieces side by side (each lane
                 // knows where its own row is); rows behind the last one are zeros
                 constexpr int P = D / 8, PER = 32 / P;  // pieces of a row, rows a step
-                const int64_t mine_at = there ? (int64_t)row * a.q_stride + (int64_t)head * D : -1;
+                const int64_t mine_at =
+                    me.there ? (int64_t)me.row * a.q_stride + (int64_t)me.head * D : -1;
                 unsigned char *dst = sq + w * C::QTILE + (t - lane) * 128;
                 if (busy) {
                     uint4 v[P];
@@ -460,13 +498,13 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 if (lane == 0) mbar_arrive(&ctl.q_ready[w]);
             }
             // pages with an id out of range, a bit each, of the next 32 / boxes tiles
-            const int32_t *table = c.page_table + (size_t)max(ln.seq[st.b], 0) * c.max_pages;
-            const int span = 32 / boxes;
+            const int span = 32 / boxes, first_edge = ln.len[st.b] / kKT - st.tile0;
             uint32_t unreadable = 0;
             int looked = 0;
             auto look = [&](int i) {
                 const int key = (st.tile0 + i) * kKT + lane * per_box;
-                const bool in = i + lane / boxes < st.n_tiles && key < tot;
+                const bool in = i + lane / boxes < st.n_tiles && key < ln.tot[st.b];
+                const int32_t *table = c.page_table + (size_t)max(ln.seq[st.b], 0) * c.max_pages;
                 unreadable = __ballot_sync(0xffffffffu, in && !page_ok(c, table[key >> sh]));
                 looked = i;
             };
@@ -491,8 +529,9 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 }
                 if (i - looked >= span) look(i);
                 const uint32_t bad = unreadable >> ((i - looked) * boxes) & ((1u << boxes) - 1);
-                const bool edge = (tile + 1) * kKT > len;
+                const bool edge = i >= first_edge;       // (tile + 1) * kKT > committed tokens
                 if (edge) {
+                    const int len = ln.len[st.b], tot = ln.tot[st.b];
                     // v's rows that must not meet the tensor core, two threads a
                     // key: rows behind the last key (0 * inf is not 0), and the
                     // infinities and NaN of drafted tokens, which only some rows
@@ -524,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                                    non_finite2<DT>(v[x].z) || non_finite2<DT>(v[x].w);
                         if (odd) {
                             atomicOr(reinterpret_cast<unsigned long long *>(
-                                         &poison[(key - len) >> 6 & 3]),
+                                         &poison()[(key - len) >> 6 & 3]),
                                      1ull << (key - len & 63));
                             __threadfence_block();
 #pragma unroll 1
@@ -541,10 +580,12 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                     uint64_t seen = ~0ull;
                     const bool masked = edge || bad;
                     if (masked) {
-                        seen = low_bits(tot - tile * kKT);
+                        const Place me = place(st, rt, NWG == 1 ? tok : token(st, rt));
+                        seen = low_bits(ln.tot[st.b] - tile * kKT);
                         for (int p = 0; p < boxes; ++p)
                             if (bad >> p & 1) seen &= ~(low_bits(per_box) << (p * per_box));
-                        seen = there ? seen_bits(tree, a.tree_words, len, tok, tile * kKT) & seen : 0ull;
+                        seen = me.there ? seen_bits(me.tree, a.tree_words, ln.len[st.b], me.tok, tile * kKT) & seen
+                                        : 0ull;
                     }
                     // scores not seen are -inf
                     auto mask = [&](uint32_t bits, uint32_t(&s)[32]) {
@@ -630,7 +671,8 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 const bool whole = now.n_tiles == now.all_tiles;
                 const float inv = l == 0.f ? 0.f : whole ? 1.f / l : 1.f;
                 float *part = piece(a, blockIdx.x, first, D, ROWS);
-                const uint64_t any = poison[0] | poison[1] | poison[2] | poison[3];
+                const Place me = place(now, rt, NWG == 1 ? tok : token(now, rt));
+                const uint64_t *odd = poison(), any = odd[0] | odd[1] | odd[2] | odd[3];
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t ob[32];
@@ -638,13 +680,13 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                     float o[32];
 #pragma unroll
                     for (int x = 0; x < 32; ++x) o[x] = __uint_as_float(ob[x]) * inv;
-                    if (any && there) {
+                    if (any && me.there) {
                         for (int k = 0; k < 4; ++k) {
-                            uint64_t bits = poison[k];
-                            bits &= tree ? (k < a.tree_words ? tree[k] : 0ull)
-                                         : low_bits(tok + 1 - k * 64);
+                            uint64_t bits = odd[k];
+                            bits &= me.tree ? (k < a.tree_words ? me.tree[k] : 0ull)
+                                            : low_bits(me.tok + 1 - k * 64);
                             for (; bits; bits &= bits - 1) {
-                                const int key = len + k * 64 + __ffsll((long long)bits) - 1;
+                                const int key = ln.len[now.b] + k * 64 + __ffsll((long long)bits) - 1;
                                 const int page =
                                     c.page_table[(size_t)ln.seq[now.b] * c.max_pages + (key >> sh)];
                                 if (!page_ok(c, page)) continue;  // (cannot be: its box was read)
@@ -668,9 +710,9 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                         for (int x = 0; x < 32; x += 4)
                             reinterpret_cast<float4 *>(part)[(size_t)(q * 8 + x / 4) * ROWS + rt] =
                                 make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-                    } else if (there) {
-                        uint4 *op = reinterpret_cast<uint4 *>(a.out + row * a.out_stride +
-                                                              (size_t)head * D + q * 32);
+                    } else if (me.there) {
+                        uint4 *op = reinterpret_cast<uint4 *>(a.out + me.row * a.out_stride +
+                                                              (size_t)me.head * D + q * 32);
 #pragma unroll
                         for (int x = 0; x < 32; x += 8)
                             op[x / 8] = make_uint4(pack2<DT>(o[x], o[x + 1]), pack2<DT>(o[x + 2], o[x + 3]),
@@ -681,8 +723,8 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 if (!whole) {
                     part[ROWS * D + rt] = m;
                     part[ROWS * (D + 1) + rt] = l;
-                } else if (there && a.lse) {
-                    a.lse[row * a.n_heads + head] =
+                } else if (me.there && a.lse) {
+                    a.lse[me.row * a.n_heads + me.head] =
                         m == -INFINITY && l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
             }
