@@ -20,6 +20,12 @@
 // with so few rows the tensor pipes keep up with the memory, and a warp's
 // registers carry a tile of scores straight into the second product. More
 // rows take the kernel of k_attention_tc.cu; plan_of has the rule.
+//
+// Measured on the device, back to back: one token of 32 heads over 1,021 tokens
+// 9.6 us, 8 tokens over 16,383 (67 MB of k and v) 26.5 us, 2.5 TB/s. Of the latter
+// 6 us pass before the first tile is there (lengths, line, page ids, tiles: reads
+// that wait for one another) and 3.4 us go to the join; the tiles between them
+// come at 4 TB/s.
 #include "attention.cuh"
 
 #include <cuda_runtime.h>
@@ -789,6 +795,9 @@ cudaError_t run_main(const AttnArgs &a, cudaStream_t s) {
 //   1 sequence of 1,021     9.6 | 14.0   9.6 | 15.6  10.3 | 16.1   - | 16.5
 //   1 sequence of 16,383   20.7 | 27.1  23.4 | 30.3  26.4 | 31.3   - | 32.1
 //   24 sequences of 3,000  58.5 | 62.9  59.7 | 64.4  75.9 | 65.6   - | 69.2
+// Above 128 rows, 256 a tile against 128 (which has two CTAs an SM, but reads k and
+// v twice): 64 tokens of 4 heads each over 32,749: 64 against 67; a batch of 16 such
+// sequences: 433 against 518.
 struct Plan {
     int rows, grid_per_sm;
     bool tc;

@@ -20,6 +20,14 @@
 // stay in registers from the maximum to the probabilities, half of the next
 // tile's are fetched meanwhile, and their product runs one tile ahead. k and v
 // are read once for 256 rows.
+//
+// What bounds it: a tile of 64 keys and 256 rows takes 1,850 to 2,150 cycles, its
+// MMAs 1,200 and its exponentials 1,024 of a scheduler's special-function unit; the
+// rest is the softmax warps' own chain (fetch 100, maximum 350 to 450, two waits of
+// 170), two warps a scheduler. Measured: 64 tokens of 32 heads over 32,749 tokens
+// 61.5 us (560 TFLOP/s; 6 us before the first scores, 7 us of joining), 16 sequences
+// with 40 to 64 tokens over 8,000 to 32,000 401 us (760 TFLOP/s; 473 us in long runs
+// at 1000 W, where the clock falls to 1.6 GHz).
 #include "attention.cuh"
 #include "umma.cuh"
 

@@ -324,6 +324,10 @@ def check_logprobs(logits, tokens, top_k, got):
     ent = torch.where(none, 0.0, ent)
     bad = torch.isnan(s0) & ~none
     logp = torch.where(none[:, None], -math.inf, z - s0.log()[:, None])
+    # the result's type is fp32, and rounding to nearest takes a magnitude of
+    # 2^128 - 2^103 (the largest number and half a step) or more to infinity: the
+    # type's lowest value under its largest one is -6.8e38
+    logp = torch.where(logp <= -(2.0 ** 128 - 2.0 ** 103), -math.inf, logp)
 
     def close(got, want, tol, what):
         got = got.double()

@@ -49,6 +49,25 @@ def test_alternatives(gpu, top_k, dtype):
     run(logits(gpu, 300, 3001, dtype, top_k), top_k=top_k)
 
 
+# CTAs of 256 threads for many rows or short ones, of 512 for few long ones
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,vocab", [(1300, 40001), (40, 40001), (3, 150001), (1300, 700)])
+def test_rows_of_every_kind_in_wide_and_narrow_blocks(gpu, rows, vocab, dtype):
+    x = logits(gpu, rows, vocab, dtype, vocab, pad=5)
+    up = torch.linspace(-9, 9, vocab, device=gpu).to(dtype)
+    x[0] = up                       # more candidates than there is room for
+    x[1] = up.flip(0)
+    x[2] = 1.5                      # equal values
+    run(x, top_k=64)
+    run(x, top_k=1)
+    x[0, :vocab // 2] = -math.inf
+    x[1] = -math.inf
+    x[2, 7] = math.inf if dtype is torch.float32 else torch.finfo(dtype).max
+    x[-1, vocab // 3:] = torch.finfo(dtype).min
+    run(x, top_k=20)
+    run(x, n_tok=700, top_k=0)
+
+
 def test_equal_values_go_by_index(gpu):
     for vocab in (100, 5000, 60000):
         x = torch.zeros((2, vocab), device=gpu, dtype=torch.bfloat16)
