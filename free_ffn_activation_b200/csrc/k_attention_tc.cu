@@ -217,6 +217,21 @@ __device__ __forceinline__ void wait_or_give_up(uint64_t *bar, uint32_t count, c
     __syncwarp();
 }
 
+// e^(score - offset) of one query row and one key, for the drafted tokens whose v
+// the tensor core must not see (offset in units of log 2). Rare, so kept out of the
+// kernel's registers.
+template <int D, int DT>
+__device__ __noinline__ float draft_weight(const uint16_t *q, const uint16_t *k, float sc, float offset) {
+    float x = 0.f;
+#pragma unroll 1
+    for (int d = 0; d < D; d += 2) {
+        const float2 a = unpack2<DT>(*reinterpret_cast<const uint32_t *>(q + d)),
+                     b = unpack2<DT>(*reinterpret_cast<const uint32_t *>(k + d));
+        x = fmaf(a.x, b.x, fmaf(a.y, b.y, x));
+    }
+    return ex2(__fsub_rn(__fmul_rn(x, sc), offset));
+}
+
 template <int D, int DT, int NWG>
 __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
     k_attention_tc(const __grid_constant__ AttnArgs a) {
@@ -698,21 +713,27 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                                 const int page =
                                     c.page_table[(size_t)ln.seq[now.b] * c.max_pages + (key >> sh)];
                                 if (!page_ok(c, page)) continue;  // (cannot be: its box was read)
-                                const uint32_t *v = reinterpret_cast<const uint32_t *>(
-                                    a.v_layer +
-                                    (((size_t)page * c.n_kv_heads + now.head) * ps + (key & (ps - 1))) * D +
-                                    q * 32);
+                                const size_t at =
+                                    (((size_t)page * c.n_kv_heads + now.head) * ps + (key & (ps - 1))) * D;
+                                // p v, so that an infinity without weight is NaN here as in
+                                // k_attention.cu (the finite elements of the row are in o)
+                                const float p = draft_weight<D, DT>(
+                                    a.q + (int64_t)me.row * a.q_stride + (int64_t)me.head * D,
+                                    c.k + (a.v_layer - c.v) + at, sc, m);
+                                const uint32_t *v =
+                                    reinterpret_cast<const uint32_t *>(a.v_layer + at + q * 32);
 #pragma unroll
                                 for (int x = 0; x < 32; x += 2) {
                                     const uint32_t vv = v[x / 2];
                                     if (!non_finite2<DT>(vv)) continue;
                                     const float2 f = unpack2<DT>(vv);
-                                    if (!isfinite(f.x)) o[x] += f.x;
-                                    if (!isfinite(f.y)) o[x + 1] += f.y;
+                                    if (!isfinite(f.x)) o[x] += p * f.x;
+                                    if (!isfinite(f.y)) o[x + 1] += p * f.y;
                                 }
                             }
                         }
                     }
+                    if (any) __syncwarp();  // (the next columns' load wants the warp together)
                     if (!whole) {
 #pragma unroll
                         for (int x = 0; x < 32; x += 4)

@@ -165,7 +165,10 @@ prox_status prox_cache_status(const prox_cache *cache, void *stream, uint32_t *f
  * with q and keys of head h and key/value head h / (n_heads / n_kv_heads).
  * A row that sees no key (and every row of an entry that is left out) gets
  * out 0 and lse -inf; what a masked key or value
- * holds (NaN and infinities among it) has no influence.
+ * holds (NaN and infinities among it) has no influence. An infinite value that
+ * is seen counts p_j v_j as any other: an infinity, or NaN where p_j is 0 (it
+ * underflows in fp32 for a drafted token, in the cache's type for a committed
+ * one; where it comes near that, parts of the keys may have seen it larger).
  * The drafted rows must be in the cache already (prox_cache_append). Rows
  * behind cu_q[n] are neither read nor written.
  *   q    : device, [rows][n_heads][head_dim] of the cache's type, rows
