@@ -18,6 +18,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kKT = 64;                   // keys of a tile
 
+// Scores in units of log 2 enter e^x as fma(score, scale, -offset) with the offset a
+// rounded product itself, so the largest one comes out as the offset's rounding
+// instead of 0. From this offset on that rounding (2^-24 of it: 8) would overflow
+// 16-bit probabilities or lose them all, and the products are rounded first: equal
+// scores then cancel exactly. Below it the exact product keeps what the scores have.
+constexpr float kRoundFirst = 134217728.f;  // 2^27
+
 #ifdef __CUDACC__
 
 __device__ __forceinline__ float ex2(float x) {

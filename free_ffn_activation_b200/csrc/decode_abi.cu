@@ -169,7 +169,8 @@ PROX_API prox_status prox_tree_attention(const prox_cache *cache, int layer, int
         return PROX_EINVAL;
     const int max_rows = max_q * (n_heads / cache->n_kv_heads);
     // (scores are kept in units of log 2, so the factor times log2(e) is used)
-    if (!(scale > 0.f) || !std::isfinite(scale * 1.44269504f)) return PROX_EINVAL;
+    const float scale_log2 = scale * 1.44269504f;
+    if (!(scale > 0.f) || !std::isfinite(scale_log2)) return PROX_EINVAL;
     if (tree && (tree_words < (max_q + 63) / 64 || tree_words > 1 << 20)) return PROX_EINVAL;
     if (n == 0 || rows == 0) return PROX_OK;
     if (!have(seqs, 4) || !have(cu_q, 4) || !have(q) || !aligned(tree, 8) || !have(out) || !aligned(lse, 4) ||
@@ -195,7 +196,7 @@ PROX_API prox_status prox_tree_attention(const prox_cache *cache, int layer, int
     a.q_stride = q_stride;
     a.tree = tree;
     a.tree_words = tree_words;
-    a.scale = scale;
+    a.scale_log2 = scale_log2;
     a.out = out;
     a.out_stride = out_stride;
     a.lse = lse;

@@ -38,7 +38,7 @@ struct AttnArgs {
     int64_t q_stride;
     const uint64_t *tree;
     int tree_words;
-    float scale;
+    float scale_log2;                       // the scale in units of log 2: scale * log2(e)
     uint16_t *out;
     int64_t out_stride;
     float *lse;

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
     // computing warps
     // ----------------------------------------------------------------------
     const int rg = wid % RG, kg = wid / RG, g = lane >> 2, tg = lane & 3;
-    const float sc = a.scale * kLog2e;
+    const float sc = a.scale_log2;
     bool live = true;
     int it = 0;
     for (int pos = begin; pos < end;) {
@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
 #pragma unroll
         for (int d = 0; d < DB; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        bool big = false;  // a row of the warp has an offset beyond kRoundFirst
 
         for (int i = 0; i < st.n_tiles; ++i, ++it) {
             const int tile = st.tile0 + i, slot = it % NST;
@@ -346,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
                 m[e] = nm;
             }
             if (__any_sync(0xffffffffu, r[0] != 1.f || r[1] != 1.f)) {
+                big = __any_sync(0xffffffffu, fmaxf(fabsf(mu[0]), fabsf(mu[1])) >= kRoundFirst);
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
                     o[d][0] *= r[0];
@@ -354,11 +356,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
                     o[d][3] *= r[1];
                 }
             }
+            if (big)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[nb][x] = __fmul_rn(s[nb][x], sc);
+            const float by = big ? 1.f : sc;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    s[nb][x] = ex2(fmaf(s[nb][x], sc, -mu[x >> 1]));
+                    s[nb][x] = ex2(fmaf(s[nb][x], by, -mu[x >> 1]));
                     l[x >> 1] += s[nb][x];
                 }
             // outputs += probabilities x v

@@ -443,7 +443,6 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         const int w = wid >> 2, t = tid & 127;
         const uint32_t lane_at = (uint32_t)(wid & 3) << 21;   // first tensor-memory lane << 16
         const uint32_t to = t_o + w * 128 + lane_at;
-        const float sc = a.scale * kLog2e;
         // tiles and stretches of the row group so far, slots used by all stretches
         uint32_t n = 0, n_full = 0, odd_stretch = 0;
         int it = 0;
@@ -521,7 +520,8 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 if (lane == 0) mbar_arrive(&ctl.q_ready[w]);
             }
             // pages with an id out of range, a bit each, of the next 32 / boxes tiles
-            const int span = 32 / boxes, first_edge = ln.len[st.b] / kKT - st.tile0;
+            const int span = 32 / boxes;
+            int first_edge = ln.len[st.b] / kKT - st.tile0;  // first tile with drafted or missing keys
             uint32_t unreadable = 0;
             int looked = 0;
             auto look = [&](int i) {
@@ -534,6 +534,9 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             look(0);
             float m = -INFINITY, l = 0.f;         // offset in use (log2 units) and sum
             uint32_t s0[32], s1[32];              // scores
+            // what the scores are multiplied with on their way into e^x: 1 once a row of
+            // the warp has an offset beyond kRoundFirst, they are scaled themselves then
+            float by = a.scale_log2;
             // tile i's buffer; its scores are there after the wait
             auto buffer = [&](int i) { return t_s + w * 128 + ((n + i) & 1) * 64 + lane_at; };
             auto formed = [&](int i) {
@@ -600,33 +603,43 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                     fence_proxy_async_smem();
                 }
                 if (busy) {
-                    uint64_t seen = ~0ull;
-                    const bool masked = edge || bad;
-                    if (masked) {
-                        const Place me = place(st, rt, NWG == 1 ? tok : token(st, rt));
-                        seen = low_bits(ln.tot[st.b] - tile * kKT);
-                        for (int p = 0; p < boxes; ++p)
-                            if (bad >> p & 1) seen &= ~(low_bits(per_box) << (p * per_box));
-                        seen = me.there ? seen_bits(me.tree, a.tree_words, ln.len[st.b], me.tok, tile * kKT) & seen
-                                        : 0ull;
-                    }
                     // scores not seen are -inf
                     auto mask = [&](uint32_t bits, uint32_t(&s)[32]) {
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
                             if (!(bits >> x & 1)) s[x] = 0xff800000u;
                     };
-                    if (masked) {
-                        mask((uint32_t)seen, s0);
-                        mask((uint32_t)(seen >> 32), s1);
-                    }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    // (once, but for the tile in which a row's offset passes kRoundFirst)
+                    for (;;) {
+                        if (i >= first_edge || bad) {
+                            const Place me = place(st, rt, NWG == 1 ? tok : token(st, rt));
+                            uint64_t seen = low_bits(ln.tot[st.b] - tile * kKT);
+                            for (int p = 0; p < boxes; ++p)
+                                if (bad >> p & 1) seen &= ~(low_bits(per_box) << (p * per_box));
+                            seen = me.there ? seen_bits(me.tree, a.tree_words, ln.len[st.b], me.tok, tile * kKT) & seen
+                                            : 0ull;
+                            mask((uint32_t)seen, s0);
+                            mask((uint32_t)(seen >> 32), s1);
+                            if (by != a.scale_log2) {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        mx[x & 3] = fmaxf(mx[x & 3], fmaxf(__uint_as_float(s0[x]), __uint_as_float(s1[x])));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                    if (__any_sync(0xffffffffu, top > m + kGrow || (top > m && m == -INFINITY))) {
+                                for (int x = 0; x < 32; ++x) {
+                                    s0[x] = __float_as_uint(__fmul_rn(__uint_as_float(s0[x]), a.scale_log2));
+                                    s1[x] = __float_as_uint(__fmul_rn(__uint_as_float(s1[x]), a.scale_log2));
+                                }
+                            }
+                        }
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            mx[x & 3] = fmaxf(mx[x & 3], fmaxf(__uint_as_float(s0[x]), __uint_as_float(s1[x])));
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * by;
+                        if (!__any_sync(0xffffffffu, top > m + kGrow || (top > m && m == -INFINITY))) break;
                         const float nm = fmaxf(m, top);
+                        if (by != 1.f && __any_sync(0xffffffffu, fabsf(nm) >= kRoundFirst && nm != -INFINITY)) {
+                            by = 1.f;
+                            first_edge = min(first_edge, i);  // (and on to the branch above from here on)
+                            continue;
+                        }
                         const float f = nm > m ? ex2(m - nm) : 1.f;
                         m = nm;
                         l *= f;
@@ -648,9 +661,10 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                                 tmem_st16(to + q * 16, o);
                             }
                         }
+                        break;
                     }
                     const float mu = m == -INFINITY ? 0.f : m;
-                    const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
+                    const float2 sc2 = make_float2(by, by), mu2 = make_float2(-mu, -mu);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     auto probabilities = [&](const uint32_t(&s)[32], uint32_t at) {
                         uint32_t p[16];
@@ -719,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                                 // k_attention.cu (the finite elements of the row are in o)
                                 const float p = draft_weight<D, DT>(
                                     a.q + (int64_t)me.row * a.q_stride + (int64_t)me.head * D,
-                                    c.k + (a.v_layer - c.v) + at, sc, m);
+                                    c.k + (a.v_layer - c.v) + at, a.scale_log2, m);
                                 const uint32_t *v =
                                     reinterpret_cast<const uint32_t *>(a.v_layer + at + q * 32);
 #pragma unroll

@@ -1,9 +1,11 @@
 """Attention of drafted tokens at the edges of its range: infinities without
-weight, against the formula in 64 bits."""
+weight, scores beyond 2^27, against the formula in 64 bits."""
 import pytest
 import torch
 
 from decode_helpers import Drafted
+from free_ffn_activation_b200 import decode as D
+from free_ffn_activation_b200 import prox as P
 
 pytestmark = pytest.mark.gpu
 TYPES = [torch.bfloat16, torch.float16]
@@ -35,3 +37,45 @@ def test_infinities_of_drafts_with_and_without_weight(gpu, group, draft, ctx, ot
     assert (first == float("inf")).all() if ctx == 0 else torch.isnan(first).all()
     assert (out[1, 0, 1::5] == float("-inf")).all()
 
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group,draft", SHAPES)
+@pytest.mark.parametrize("power", [10, 13, 14, 15])
+def test_scores_far_beyond_a_million(gpu, group, draft, dtype, power):
+    """q . k exact in fp32 and so far apart that the largest one takes all: the
+    result is its v, or the mean of the two that share it. (Scores up to
+    2^(7 + 2 power) / 8, in units of log 2 with a rounding of 2^-24 of that, which
+    must not reach e^x.)"""
+    ctx = 700
+    c = Drafted(gpu, [ctx, 90], [draft, draft], group=group, dtype=dtype, seed=power)
+    heads = torch.arange(c.q.shape[1], device=gpu)
+    # (finer than powers of two: their products with the scale would be exact)
+    c.q.copy_((1.0 + heads / 64.0)[None, :, None] * 2.0 ** power)
+    for s in range(2):
+        n = c.lens[s] + draft
+        rank = torch.randperm(c.lens[s], device=gpu, generator=torch.Generator(gpu).manual_seed(s))
+        rank = (rank // 2 + 1).float() / (c.lens[s] // 2 + 1)          # pairs share a score
+        level = torch.cat([rank, torch.full((draft,), -1.0, device=gpu)])
+        pos = torch.arange(n, device=gpu)
+        pages = c.cache.page_table[s].long()[pos // 16]
+        for h in range(2):
+            c.cache.k[0][pages, h, pos % 16] = ((level * 60).round() / 64 * 2.0 ** power)[:, None].to(dtype)
+    out, lse = c.run()
+    torch.cuda.synchronize()
+    for i, s in enumerate((0, 1)):
+        k, v = c.rows_of(s)
+        for h in range(c.q.shape[1]):
+            kh, vh = k[h // group], v[h // group]
+            top = kh[:, 0] == kh[:, 0].max()
+            assert top[:c.lens[s]].any() and not top[c.lens[s]:].any()
+            want = vh[top].mean(0)
+            # the keys at the top share one probability (1 up to the rounding of the
+            # offset), which is rounded to the output's type, as is the result; the
+            # sums are off by 2^-22 at most
+            u = torch.finfo(dtype).eps / 2
+            tol = (2 * u + u * u) * want.abs() + 2.0 ** -22 * vh[top].abs().mean(0)
+            got = out[c.cu_host[i]:c.cu_host[i + 1], h].double()
+            assert ((got - want).abs() <= tol).all(), (s, h, (got - want).abs().max())
+            x = float(c.q[0, h].double() @ kh[top][0]) * c.scale
+            assert ((lse[c.cu_host[i]:c.cu_host[i + 1], h].double() - x).abs() <= abs(x) * 2.0 ** -21).all()
+    assert D.cache_status(c.cache) == (P.PROX_OK, 0)
