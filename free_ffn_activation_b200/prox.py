@@ -514,7 +514,7 @@ def static_last_device_status(device=None) -> tuple[int, int]:
     return st, flags.value
 
 
-SKIP_OFF, SKIP_STAGE1_TC, SKIP_STAGE2_TC, SKIP_ATTENTION = 0, 1, 3, 4
+SKIP_OFF, SKIP_STAGE1_TC, SKIP_STAGE2_TC, SKIP_ATTENTION, SKIP_ATTENTION_OUTPUTS = 0, 1, 3, 4, 5
 
 
 def test_set_skip(where: int, position: int = -1) -> None:

@@ -48,6 +48,9 @@ void prox_test_set_stamps(unsigned long long *slots);
  *      step `position` (status bit 5);
  *   4  tree attention: the loading warp of CTA 0 never fills its slot
  *      `position` (PROX_CACHE_TIMEOUT in the cache's status word);
+ *   5  tree attention in tensor memory: the softmax warps of CTA 0 give up the
+ *      wait for the outputs of their stretch `position` at once, with products
+ *      under way (PROX_CACHE_TIMEOUT in the cache's status word);
  *   0  off.
  * Nothing faults: the kernel records the timeout in the status word, skips
  * the rest of its MMAs, waits (with the default bound) for those already

@@ -1,5 +1,5 @@
 """Attention of drafted tokens at the edges of its range: infinities without
-weight, scores beyond 2^27, against the formula in 64 bits."""
+weight, scores beyond 2^27, against the formula in 64 bits; waits that give up."""
 import pytest
 import torch
 
@@ -79,3 +79,27 @@ def test_scores_far_beyond_a_million(gpu, group, draft, dtype, power):
             x = float(c.q[0, h].double() @ kh[top][0]) * c.scale
             assert ((lse[c.cu_host[i]:c.cu_host[i + 1], h].double() - x).abs() <= abs(x) * 2.0 ** -21).all()
     assert D.cache_status(c.cache) == (P.PROX_OK, 0)
+
+
+# row tiles of 128 and of 256 rows, and the second group of 128 with few rows
+@pytest.mark.parametrize("group,draft", [(4, 20), (4, 60), (4, 33), (8, 40)])
+@pytest.mark.parametrize("position", [0, 1])
+def test_a_wait_for_outputs_that_gives_up_is_reported(gpu, group, draft, position):
+    """Products are under way when the softmax stops waiting for them: they end before
+    the block gives its tensor memory back, the call ends with an error, and the
+    calls behind it are right."""
+    c = Drafted(gpu, [30000, 600, 9], [draft] * 3, group=group, kv_heads=1, page=32, tree="random")
+    want = c.run()
+    for _ in range(10):
+        P.test_set_skip(P.SKIP_ATTENTION_OUTPUTS, position)
+        try:
+            c.run()
+        finally:
+            P.test_set_skip(P.SKIP_OFF)
+        again = c.run()
+        torch.cuda.synchronize()
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+        st = D.cache_status(c.cache)
+        # (a block's run may lie in one stretch: then there is no second one)
+        assert st == (P.PROX_ETIMEOUT, D.CACHE_TIMEOUT) or position == 1 and st == (P.PROX_OK, 0)
+    c.check(*want)
