@@ -136,8 +136,11 @@ PROX_API prox_status prox_cache_status(const prox_cache *cache, void *stream, ui
     cudaStream_t st = (cudaStream_t)stream;
     uint32_t v = 0;
     if (cudaMemcpyAsync(&v, cache->status, sizeof v, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-        cudaMemsetAsync(cache->status, 0, sizeof v, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
+        return PROX_ECUDA;
+    // (only what was read is cleared: calls on other streams may set bits meanwhile)
+    if (v && (launch_cache_clear(*cache, v, st) != cudaSuccess ||
+              cudaStreamSynchronize(st) != cudaSuccess))
         return PROX_ECUDA;
     if (flags_out) *flags_out = v;
     return v & PROX_CACHE_TIMEOUT ? PROX_ETIMEOUT : v ? PROX_EDATA : PROX_OK;

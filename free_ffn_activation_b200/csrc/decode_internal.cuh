@@ -15,6 +15,8 @@ constexpr int kMaxDraft = 256;      // drafted tokens of one sequence
 
 // page operations (k_cache.cu)
 cudaError_t launch_cache_init(const prox_cache &c, cudaStream_t s);
+// takes `bits` off the status word
+cudaError_t launch_cache_clear(const prox_cache &c, uint32_t bits, cudaStream_t s);
 cudaError_t launch_cache_reserve(const prox_cache &c, int n, const int32_t *seqs,
                                  const int32_t *n_new, uint8_t *ok, cudaStream_t s);
 cudaError_t launch_cache_append(const prox_cache &c, int layer, int n, const int32_t *seqs,

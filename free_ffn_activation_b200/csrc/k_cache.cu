@@ -188,6 +188,12 @@ __global__ void __launch_bounds__(256) k_cache_init(const prox_cache c) {
     }
 }
 
+__global__ void k_cache_clear(const prox_cache c, uint32_t bits) {
+    pdl_wait();
+    pdl_launch();
+    atomicAnd(c.status, ~bits);
+}
+
 // ---------------------------------------------------------------------------
 // reserve
 // ---------------------------------------------------------------------------
@@ -799,6 +805,10 @@ cudaError_t book(void (*kern)(P...), int ctas, int block, size_t smem, cudaStrea
 
 cudaError_t launch_cache_init(const prox_cache &c, cudaStream_t s) {
     return launch(k_cache_init, dim3(64), 256, 0, s, c);
+}
+
+cudaError_t launch_cache_clear(const prox_cache &c, uint32_t bits, cudaStream_t s) {
+    return launch(k_cache_clear, dim3(1), 1, 0, s, c, bits);
 }
 
 cudaError_t launch_cache_reserve(const prox_cache &c, int n, const int32_t *seqs,

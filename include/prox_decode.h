@@ -147,8 +147,9 @@ prox_status prox_cache_compact(const prox_cache *cache, int n, const int32_t *se
 prox_status prox_cache_free(const prox_cache *cache, int n, const int32_t *seqs, void *stream);
 
 /*
- * prox_cache_status -- reads and clears the cache's status word (synchronises
- * `stream`). PROX_ETIMEOUT if a wait gave up since the last read, else
+ * prox_cache_status -- reads the cache's status word and clears the bits that it
+ * returns (synchronises `stream`; a bit that a call on another stream sets
+ * meanwhile is returned now or by the next call). PROX_ETIMEOUT if a wait gave up since the last read, else
  * PROX_EDATA if another bit was set, else PROX_OK; *flags_out (host, may be NULL) receives the bits.
  */
 prox_status prox_cache_status(const prox_cache *cache, void *stream, uint32_t *flags_out);

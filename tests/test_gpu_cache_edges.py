@@ -1,0 +1,45 @@
+"""The cache's status word under calls on two streams."""
+import random
+
+import pytest
+import torch
+
+from decode_helpers import Drafted
+from free_ffn_activation_b200 import decode as D
+from free_ffn_activation_b200 import prox as P
+
+pytestmark = pytest.mark.gpu
+
+
+def test_status_bits_set_while_the_word_is_read_are_kept(gpu):
+    """An attention call on another stream sets a bit at some time while the word
+    is read again and again: one of the reads must return it."""
+    c = Drafted(gpu, [3], [1])
+    c.seqs.fill_(99)
+    ws = D.attention_workspace(c.cache, 1, 8)
+    out, lse = c.run(ws=ws)
+    assert D.cache_status(c.cache)[1] == D.CACHE_BAD_SEQ
+    side, rng, lost = torch.cuda.Stream(), random.Random(1), 0
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(400):
+        done = torch.cuda.Event()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(rng.randrange(1000, 200000))
+            c.run(out=out, lse=lse, ws=ws)
+            done.record()
+        bits = 0
+        while not done.query():
+            bits |= D.cache_status(c.cache)[1]
+        done.synchronize()
+        bits |= D.cache_status(c.cache)[1]
+        lost += bits != D.CACHE_BAD_SEQ
+    assert lost == 0
+
+
+def test_status_returns_and_clears_what_was_set(gpu):
+    c = Drafted(gpu, [3], [1])
+    for bits, st in ((0, P.PROX_OK), (D.CACHE_FULL | D.CACHE_BAD_ARG, D.PROX_EDATA),
+                     (D.CACHE_TIMEOUT | D.CACHE_BAD_SEQ, P.PROX_ETIMEOUT)):
+        c.cache.status.fill_(bits)
+        assert D.cache_status(c.cache) == (st, bits)
+        assert int(c.cache.status) == 0 and D.cache_status(c.cache) == (P.PROX_OK, 0)
