@@ -87,8 +87,9 @@ size_t prox_cache_workspace_bytes(const prox_cache *cache);
 /*
  * prox_cache_reserve -- pages for n_new more tokens behind the committed ones:
  * sequence seqs[i] holds at least ceil((length + n_new[i]) / page_size) pages
- * afterwards. Entries take pages in their order; one that does not fit (free
- * pages, or max_pages columns) gets none, as do those behind it that need any.
+ * afterwards. Entries take pages in their order; one that finds too few free
+ * pages gets none, as do those behind it that need any. One that needs more than
+ * max_pages columns gets none either, and takes nothing from those behind it.
  *   seqs, n_new : device, int32 [n], 0 <= n <= max_seqs, each sequence once.
  *   ok          : device, uint8 [n], 1 = the entry has its pages, 0 = it was
  *                 refused or left out; or NULL.

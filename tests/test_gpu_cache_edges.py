@@ -1,10 +1,11 @@
-"""The cache's status word under calls on two streams."""
+"""Page operations on lists they have to refuse in part, and the status word under
+calls on two streams."""
 import random
 
 import pytest
 import torch
 
-from decode_helpers import Drafted
+from decode_helpers import Drafted, ints
 from free_ffn_activation_b200 import decode as D
 from free_ffn_activation_b200 import prox as P
 
@@ -43,3 +44,21 @@ def test_status_returns_and_clears_what_was_set(gpu):
         c.cache.status.fill_(bits)
         assert D.cache_status(c.cache) == (st, bits)
         assert int(c.cache.status) == 0 and D.cache_status(c.cache) == (P.PROX_OK, 0)
+
+
+def test_reserve_refuses_too_many_columns_alone_and_too_few_pages_in_order(gpu):
+    """ok[] by hand: an entry that needs more columns than the table has is refused
+    alone; one that finds too few free pages, and those behind it that need any."""
+    c = D.PagedCache(1, 6, 1, 16, 64, 8, 3, torch.bfloat16, gpu)
+
+    def reserve(seqs, n_new):
+        ok = torch.full((len(seqs),), 7, dtype=torch.uint8, device=gpu)
+        D.cache_reserve(c, ints(seqs, gpu), ints(n_new, gpu), ok)
+        torch.cuda.synchronize()
+        return ok.tolist(), c.held[seqs].tolist(), D.cache_status(c)[1]
+
+    assert reserve([0, 1, 2], [49, 1, 0]) == ([0, 1, 1], [0, 1, 0], D.CACHE_FULL)
+    assert reserve([3, 4, 5, 6, 7], [48, 33, 1, 0, 16]) == ([1, 0, 0, 1, 0], [3, 0, 0, 0, 0], D.CACHE_FULL)
+    # both in one call: the one that is too wide takes no page from the others' count
+    assert reserve([4, 5, 6], [1000, 32, 1]) == ([0, 1, 0], [0, 2, 0], D.CACHE_FULL)
+    assert int(c.n_free) == 0
