@@ -648,6 +648,15 @@ __device__ int check_path(const prox_cache &c, int n, const int32_t *seqs, const
         if (flag && threadIdx.x == 0) atomicOr(c.status, PROX_CACHE_BAD_ARG);
         return -1;
     }
+    const int32_t *table = c.page_table + (size_t)s * c.max_pages;
+    for (int j = threadIdx.x; j < m; j += blockDim.x)
+        bad |= !page_ok(c, table[(st->len + path[(size_t)i * max_path + j]) / c.page_size]) ||
+               !page_ok(c, table[(st->len + j) / c.page_size]);
+    bad = __syncthreads_or(bad);
+    if (bad) {
+        if (flag && threadIdx.x == 0) atomicOr(c.status, PROX_CACHE_BAD_STATE);
+        return -1;
+    }
     *count = m;
     return s;
 }
@@ -671,11 +680,9 @@ __global__ void __launch_bounds__(256)
     for (int j = threadIdx.x; j < m; j += blockDim.x) {
         const int a = st.len + path[(size_t)i * max_path + j], b = st.len + j;
         const int pa = table[a / ps], pb = table[b / ps];
-        const bool good = page_ok(c, pa) && page_ok(c, pb);
-        if (!good) atomicOr(c.status, PROX_CACHE_BAD_STATE);
         // (n_pages * page_size fits in 31 bits)
-        s_from[j] = good && a != b ? pa * ps + a % ps : -1;
-        s_to[j] = good ? pb * ps + b % ps : 0;
+        s_from[j] = a != b ? pa * ps + a % ps : -1;
+        s_to[j] = pb * ps + b % ps;
     }
     __syncthreads();
     const int lanes = c.head_dim / 8;                  // 8 or 16

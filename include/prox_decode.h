@@ -134,7 +134,8 @@ prox_status prox_cache_fork(const prox_cache *cache, int n, const int32_t *src, 
  *   path   : device, int32 [n][max_path], 1 <= max_path <= 256.
  *   n_path : device, int32 [n], 0 <= n_path[i] <= max_path.
  *   ok     : device, uint8 [n] or NULL; an entry whose path is not strictly
- *            ascending or leaves the held pages is refused as a whole.
+ *            ascending, leaves the held pages or meets a page id out of range is
+ *            refused as a whole.
  */
 prox_status prox_cache_compact(const prox_cache *cache, int n, const int32_t *seqs,
                                const int32_t *path, int max_path, const int32_t *n_path,

@@ -1,5 +1,5 @@
-"""Page operations on lists they have to refuse in part, and the status word under
-calls on two streams."""
+"""Page operations on lists they have to refuse in part, on state that is out of
+range, and the status word under calls on two streams."""
 import random
 
 import pytest
@@ -44,6 +44,34 @@ def test_status_returns_and_clears_what_was_set(gpu):
         c.cache.status.fill_(bits)
         assert D.cache_status(c.cache) == (st, bits)
         assert int(c.cache.status) == 0 and D.cache_status(c.cache) == (P.PROX_OK, 0)
+
+
+def test_paths_over_unreadable_pages_are_refused(gpu):
+    c = D.PagedCache(2, 20, 2, 16, 64, 4, 4, torch.bfloat16, gpu)
+    for t in (c.k, c.v):
+        t.copy_(torch.randn(t.shape, device=gpu).bfloat16())
+    D.cache_reserve(c, ints([0, 1, 2, 3], gpu), ints([48] * 4, gpu))
+    c.length.copy_(ints([30, 30, 30, 30], gpu))
+    c.page_table[0, 2] = 20                 # rows 32 .. 47 of these
+    c.page_table[1, 2] = -1
+    c.page_table[3, 2] = 10 ** 9
+    k, v = c.k.clone(), c.v.clone()
+    ok = torch.full((4,), 7, dtype=torch.uint8, device=gpu)
+    # read from such a page; written to one; neither; not touched by the path
+    path = ints([[2, 0, 0], [0, 1, 3], [1, 4, 9], [1, 0, 0]], gpu)
+    D.cache_compact(c, ints([0, 1, 2, 3], gpu), path, ints([1, 3, 3, 1], gpu), ok)
+    torch.cuda.synchronize()
+    assert ok.tolist() == [0, 0, 1, 1] and c.length.tolist() == [30, 30, 33, 31]
+    assert D.cache_status(c) == (D.PROX_EDATA, D.CACHE_BAD_STATE)
+    for new, old in ((c.k, k), (c.v, v)):
+        def row(s, pos):
+            return int(c.page_table[s, pos // 16]), pos % 16
+        for s, pairs in ((2, ((30, 31), (31, 34), (32, 39))), (3, ((30, 31),))):
+            for to, at in pairs:
+                (p, o), (q, r) = row(s, to), row(s, at)
+                assert torch.equal(new[:, p, :, o], old[:, q, :, r])
+                old[:, p, :, o] = old[:, q, :, r].clone() if (s, to) != (2, 31) else new[:, p, :, o]
+        assert torch.equal(new, old)        # and nothing else moved
 
 
 def test_reserve_refuses_too_many_columns_alone_and_too_few_pages_in_order(gpu):
