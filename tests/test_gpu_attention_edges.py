@@ -1,9 +1,10 @@
 """Attention of drafted tokens at the edges of its range: infinities without
-weight, scores beyond 2^27, against the formula in 64 bits; waits that give up."""
+weight, scores beyond 2^27, many row tiles, offsets that have to be cut, against
+the formula in 64 bits; waits that give up."""
 import pytest
 import torch
 
-from decode_helpers import Drafted
+from decode_helpers import Drafted, check_attention, ints
 from free_ffn_activation_b200 import decode as D
 from free_ffn_activation_b200 import prox as P
 
@@ -103,3 +104,54 @@ def test_a_wait_for_outputs_that_gives_up_is_reported(gpu, group, draft, positio
         # (a block's run may lie in one stretch: then there is no second one)
         assert st == (P.PROX_ETIMEOUT, D.CACHE_TIMEOUT) or position == 1 and st == (P.PROX_OK, 0)
     c.check(*want)
+
+
+# rows of a key/value head beyond two tiles of 256: up to 64 tiles
+@pytest.mark.parametrize("dim,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+@pytest.mark.parametrize("group,draft", [(3, 171), (4, 256), (8, 160), (8, 256), (64, 256)])
+def test_many_row_tiles(gpu, group, draft, dim, dtype):
+    c = Drafted(gpu, [70, 1000], [draft, draft - 37], group=group, kv_heads=1, dim=dim, dtype=dtype, page=64,
+                tree="random", seed=group)
+    c.check(*c.run())
+    # one sequence alone: its tiles are cut over the blocks
+    c = Drafted(gpu, [5000], [draft], group=group, kv_heads=1, dim=dim, dtype=dtype, page=128, seed=group)
+    c.check(*c.run())
+    assert D.cache_status(c.cache) == (P.PROX_OK, 0)
+
+
+@pytest.mark.parametrize("group,draft", [(4, 4), (2, 12), (4, 20), (4, 70)])
+def test_offsets_that_are_cut_leave_the_other_rows(gpu, group, draft):
+    """Rows up to the cut follow the formula; rows behind it, and the gaps between
+    rows, keep what they hold."""
+    c = Drafted(gpu, [30], [draft], group=group, extra_rows=5)
+    heads = c.q.shape[1]
+
+    def run(cu, max_q):
+        c.cu, c.max_q = ints(cu, gpu), max_q
+        c.seqs = ints([0] * (len(cu) - 1), gpu)
+        wide = torch.full((draft + 5, heads + 3, 128), 3.0, dtype=c.q.dtype, device=gpu)
+        lse = torch.full((draft + 5, heads), 7.0, device=gpu)
+        c.run(out=wide[:, :heads], lse=lse)
+        torch.cuda.synchronize()
+        assert (wide[:, heads:] == 3).all()
+        return wide[:, :heads], lse, D.cache_status(c.cache)[1]
+
+    def check(out, lse, a, b, flags):
+        """Rows a .. b - 1 are a chain of b - a drafted tokens, the others untouched."""
+        k, v = (x[:, :30 + b - a] for x in c.rows_of(0))
+        seen = torch.ones((b - a, 30 + b - a), dtype=torch.bool, device=gpu).tril(30)
+        check_attention(out[a:b], lse[a:b], c.q[a:b], k, v, seen, c.scale)
+        rest = torch.ones(draft + 5, dtype=torch.bool, device=gpu)
+        rest[a:b] = False
+        assert (out[rest] == 3).all() and (lse[rest] == 7).all()
+        assert flags == D.CACHE_BAD_ARG
+
+    for cu, first in (([0, 10 ** 6], 0),            # behind the tensor's last row
+                      ([0, draft + 5], 0),          # more than max_q
+                      ([-3, draft], 0),             # before its first row
+                      ([2, draft, -1, 0], 2)):      # descending: no rows
+        out, lse, flags = run(cu, draft)
+        check(out, lse, first, draft, flags)
+    for cu in ([draft, -2], [10 ** 6, 10 ** 6], [-5, -1], [-2 ** 31, -2 ** 31 + 1]):
+        out, lse, flags = run(cu, draft)
+        assert (out == 3).all() and (lse == 7).all() and flags == D.CACHE_BAD_ARG, cu
