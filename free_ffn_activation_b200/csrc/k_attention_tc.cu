@@ -64,7 +64,7 @@ static_assert(sizeof(Line) % 16 == 0, "barriers are 8-byte aligned");
 struct Ctl {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     // per row group: q written; scores there and probabilities there (two
-    // buffers); a tile's second product done, and that of a stretch's last tile
+    // buffers); the second products of a stretch done but for its last tile's, and all
     uint64_t q_ready[2], s_full[2][2], p_ready[2][2], o_done[2], o_full[2];
     uint64_t poison[2][4];          // drafted tokens whose v has an infinity or NaN (by stretch parity)
     uint64_t drained[2];            // all of a row group's MMAs are done
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                     for (int k = 0; k < kKT / 16; ++k)
                         umma_ts(d_o, d_s + buf * 64 + k * 8, hi | (v0 + k * (2048 >> 4)), pv_idesc,
                                 k > 0 || i > 0);
-                    umma_commit(&ctl.o_done[w]);
+                    if (i + 2 == n_tiles || n_tiles == 1) umma_commit(&ctl.o_done[w]);
                     if (i + 1 == n_tiles) umma_commit(&ctl.o_full[w]);
                 }
                 if (more) qk();
@@ -647,13 +647,14 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                         m = nm;
                         l *= f;
                         if (i > 0) {
-                            // Products up to the last tile's are in the outputs then. (A
-                            // wait tells a phase by its parity: tile i's scores were
-                            // formed behind the product of tile i - 2, and tile i's own
-                            // product waits for this thread, so it is the phase of tile
-                            // i - 1 or the one behind it that is under way.)
-                            wait_or_give_up(&ctl.o_done[w], n + i - 1, a, ctl, live);
-                            tc_fence_after();
+                            // The last tile's product is in the outputs once the next
+                            // tile's scores are formed, which come behind it.
+                            if (i + 1 < st.n_tiles) {
+                                formed(i + 1);
+                            } else {
+                                wait_or_give_up(&ctl.o_done[w], n_full, a, ctl, live);
+                                tc_fence_after();
+                            }
 #pragma unroll 1
                             for (int q = 0; q < D / 16; ++q) {
                                 uint32_t o[16];
@@ -710,6 +711,8 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                 ctl.dead = 1;
                 atomicOr(c.status, PROX_CACHE_TIMEOUT);
             }
+            // (a wait tells a phase by its parity, so every phase is waited for)
+            wait_or_give_up(&ctl.o_done[w], n_full, a, ctl, live);
             wait_or_give_up(&ctl.o_full[w], n_full++, a, ctl, live);
             tc_fence_after();
             if (busy) {

@@ -155,3 +155,21 @@ def test_offsets_that_are_cut_leave_the_other_rows(gpu, group, draft):
     for cu in ([draft, -2], [10 ** 6, 10 ** 6], [-5, -1], [-2 ** 31, -2 ** 31 + 1]):
         out, lse, flags = run(cu, draft)
         assert (out == 3).all() and (lse == 7).all() and flags == D.CACHE_BAD_ARG, cu
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group,draft", SHAPES)
+def test_maxima_that_grow_from_tile_to_tile(gpu, group, draft, dtype):
+    """Every tile of 64 keys raises a row's maximum by more than 2^8, the last one
+    (drafted keys) too, in runs of many tiles: outputs are rescaled before each."""
+    ctx, n = 500, 70
+    c = Drafted(gpu, [ctx] * n, [draft] * n, group=group, kv_heads=4, dtype=dtype, page=64, seed=draft)
+    c.q.mul_(0.05).add_(1.0)
+    pos = torch.arange(ctx + draft, device=gpu)
+    # a mean of pos / 100 over 128 elements: scores of 0.11 a key, 10 log2 units a tile
+    for s in range(n):
+        pages = c.cache.page_table[s].long()[pos // 64]
+        for h in range(4):
+            c.cache.k[0][pages, h, pos % 64] += (pos / 100.0)[:, None].to(dtype)
+    c.check(*c.run())
+    assert D.cache_status(c.cache) == (P.PROX_OK, 0)
