@@ -218,14 +218,18 @@ __device__ __forceinline__ void wait_or_give_up(uint64_t *bar, uint32_t count, c
 }
 
 // e^(score - offset) of one query row and one key, for the drafted tokens whose v
-// the tensor core must not see (offset in units of log 2). Rare, so kept out of the
-// kernel's registers.
+// the tensor core must not see (offset in units of log 2). q is a row group's tile in
+// shared memory (a row's output may lie where the row was read from), t the row. Rare,
+// so kept out of the kernel's registers.
 template <int D, int DT>
-__device__ __noinline__ float draft_weight(const uint16_t *q, const uint16_t *k, float sc, float offset) {
+__device__ __noinline__ float draft_weight(const unsigned char *q, int t, const uint16_t *k, float sc,
+                                           float offset) {
     float x = 0.f;
 #pragma unroll 1
     for (int d = 0; d < D; d += 2) {
-        const float2 a = unpack2<DT>(*reinterpret_cast<const uint32_t *>(q + d)),
+        const int y = d >> 3;  // 16-byte piece
+        const float2 a = unpack2<DT>(*reinterpret_cast<const uint32_t *>(
+                         q + t * 128 + (y >> 3) * (128 * 128) + (((y & 7) ^ (t & 7)) << 4) + (d & 7) * 2)),
                      b = unpack2<DT>(*reinterpret_cast<const uint32_t *>(k + d));
         x = fmaf(a.x, b.x, fmaf(a.y, b.y, x));
     }
@@ -743,8 +747,7 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
                                 // p v, so that an infinity without weight is NaN here as in
                                 // k_attention.cu (the finite elements of the row are in o)
                                 const float p = draft_weight<D, DT>(
-                                    a.q + (int64_t)me.row * a.q_stride + (int64_t)me.head * D,
-                                    c.k + (a.v_layer - c.v) + at, a.scale_log2, m);
+                                    sq + w * C::QTILE, t, c.k + (a.v_layer - c.v) + at, a.scale_log2, m);
                                 const uint32_t *v =
                                     reinterpret_cast<const uint32_t *>(a.v_layer + at + q * 32);
 #pragma unroll

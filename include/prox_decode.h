@@ -187,7 +187,10 @@ prox_status prox_cache_status(const prox_cache *cache, void *stream, uint32_t *f
  *   ws   : device, prox_attention_workspace_bytes(...) bytes, needs no
  *          clearing; calls that overlap on the device need one each.
  * Arithmetic: scores, softmax statistics and sums in fp32; the probabilities
- * are rounded to the cache's type for the product with v.
+ * are rounded to the cache's type for the product with v. The sums are divided
+ * at the end: |v| * 2^8 * (keys that a row sees) has to stay below 2^128.
+ * `out` may be `q` itself (the same rows); otherwise no output overlaps what
+ * the call reads.
  * A sequence may be listed several times. n <= 65536, n_heads a multiple of
  * n_kv_heads, n_heads <= 64 * n_kv_heads; n_kv_heads * (max_pages * page_size
  * / 64 + 1) < 2^31 / 64.

@@ -173,3 +173,19 @@ def test_maxima_that_grow_from_tile_to_tile(gpu, group, draft, dtype):
             c.cache.k[0][pages, h, pos % 64] += (pos / 100.0)[:, None].to(dtype)
     c.check(*c.run())
     assert D.cache_status(c.cache) == (P.PROX_OK, 0)
+
+
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("group,draft", SHAPES)
+def test_outputs_in_the_place_of_the_queries(gpu, group, draft, odd):
+    for lens in ([3000, 61], [200] * 60):
+        c = Drafted(gpu, lens, [draft] * len(lens), group=group, tree="random", seed=draft)
+        if odd:                             # a visible infinity in v of some drafted tokens
+            p, o = int(c.cache.page_table[1, lens[1] // 16]), lens[1] % 16
+            c.cache.v[0, p, :, o, ::3] = float("inf")
+        want, wlse = c.run()
+        c.check(want, wlse)
+        got, lse = c.run(out=c.q)
+        torch.cuda.synchronize()
+        same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))  # noqa: E731
+        assert got.data_ptr() == c.q.data_ptr() and same(got.contiguous(), want) and torch.equal(lse, wlse)
