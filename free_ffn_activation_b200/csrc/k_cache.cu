@@ -23,9 +23,16 @@ namespace {
 
 // Shapes of a bookkeeping call: few entries that can list few pages (by the page
 // table's width) run on 8 CTAs of 256 threads, others on 16 of 1024. Fork and
-// free of 8 sequences of 50 pages: 16 against 19 us; of 32 of 2,500: 138 against
-// 41 us.
-constexpr int kFew = 256, kFewPages = 1 << 14, kFewCtas = 8;
+// free on the device (us; 8 of 256 | 16 of 1024), by entries x pages of each:
+//   8 x 50      15.5 |  17.6     32 x 50     16.0 | 19.8     128 x 20    19.4 | 20.4
+//   8 x 200     16.1 |  18.6     32 x 250    25.5 | 19.4     128 x 100   38.6 | 20.2
+//   8 x 1,000   23.7 |  19.2     32 x 500    36.4 | 19.6     256 x 4     25.9 | 19.7
+//   8 x 2,000   32.6 |  19.8     32 x 2,500 115.6 | 31.1     256 x 64    38.7 | 20.4
+// The shapes cross between 2,600 and 8,000 pages, and by 256 entries for any pages.
+// (A wide table of short sequences costs the larger shape's 2 us, a full one of 16,000
+// pages cost the smaller one 16.)
+constexpr int kFew = 256;              // entries that the smaller shape has room for
+constexpr int kFewEntries = 128, kFewPages = 4096, kFewCtas = 8;
 constexpr int kSome = 1024, kCtas = 16;
 constexpr int kWindow = 8192;          // chunks of a CTA whose owners and masks are kept
 
@@ -801,7 +808,7 @@ cudaError_t book(void (*kern)(P...), int ctas, int block, size_t smem, cudaStrea
 
 // the kernel's shape for n entries of cache c (see kFew)
 #define BOOK(kern, more, c, n, ...)                                                               \
-    ((n) <= kFew && (long)(n) * (c).max_pages <= kFewPages                                        \
+    ((n) <= kFewEntries && (long)(n) * (c).max_pages <= kFewPages                                  \
          ? book(kern<256, kFew>, kFewCtas, 256, sizeof(Book<kFew>) + (more), s, c, n, __VA_ARGS__) \
      : (n) <= kSome                                                                               \
          ? book(kern<1024, kSome>, kCtas, 1024, sizeof(Book<kSome>) + (more), s, c, n, __VA_ARGS__) \
