@@ -566,9 +566,10 @@ __device__ int joining_cuts(const Line &ln, const AttnArgs &a, int ROWS, Cuts &c
 // first cut in it. The CTAs share out steps of 32 rows and CC columns: lanes are
 // rows (a piece is read in runs of 512 bytes), the pieces are dealt out to the
 // warps, whose sums meet in shared memory in a fixed order. All reads of BATCH
-// pieces a warp are in flight at once. What has to be joined is worked out while
-// the main kernel still runs (notes that its CTAs left in the workspace instead
-// cost two more reads behind it: 11.4 against 9.8 us for one token over 1,021).
+// pieces a warp are in flight at once. What has to be joined is worked out before
+// the wait for the main kernel: on an SM whose CTAs of that kernel have ended (beside
+// them its registers leave no room). Notes that its CTAs left in the workspace instead
+// cost two more reads behind it: 11.4 against 9.8 us for one token over 1,021.
 template <int D, int DT, int CC, int BATCH>
 __global__ void __launch_bounds__(256, BATCH > 2 ? 1 : 2)
     k_attention_join(const __grid_constant__ AttnArgs a, int ROWS) {
@@ -805,9 +806,19 @@ cudaError_t run_main(const AttnArgs &a, cudaStream_t s) {
 //   1 sequence of 1,021     9.6 | 14.0   9.6 | 15.6  10.3 | 16.1   - | 16.5
 //   1 sequence of 16,383   20.7 | 27.1  23.4 | 30.3  26.4 | 31.3   - | 32.1
 //   24 sequences of 3,000  58.5 | 62.9  59.7 | 64.4  75.9 | 65.6   - | 69.2
-// Above 128 rows, 256 a tile against 128 (which has two CTAs an SM, but reads k and
-// v twice): 64 tokens of 4 heads each over 32,749: 64 against 67; a batch of 16 such
-// sequences: 433 against 518.
+// The same holds with 2 key/value heads (one of 16,383: 14.0 | 16.7 with 4 rows, 17.8
+// | 22.4 with 32; 24 of 3,000: 23.3 | 32.0 and 28.7 | 35.2, above the rule's border
+// only in the last), with dim 64 (15.7 | 20.0, 19.0 | 20.5; 42.5 | 44.7, 54.0 | 44.9)
+// and with 16-token pages (20.5 | 26.0, 25.6 | 30.6; 58.2 | 63.9, 72.4 | 66.8).
+// Tiles of 128 | 256 rows (the former have two CTAs an SM, but read k and v again for
+// each 128 rows), by dim and key/value heads:
+//                                      128, 8         64, 8         128, 2
+//   1 of 16,383, 48 rows            31.5 | 34.0   20.0 | 28.1   23.2 | 23.3
+//   24 of 3,000, 128 rows           75.6 | 93.2   54.5 | 75.3   38.4 | 32.7
+//   1 of 32,749, 256 rows           62.3 | 59.6   45.9 | 50.4   30.9 | 34.0
+//   16 of 8,000, 192 rows          192.9 | 158.2 132.8 | 138.9  67.9 | 65.0
+// More than 128 rows take 256 for the batches of dim 128; dim 64 would gain 4 to 9%
+// by 128.
 struct Plan {
     int rows, grid_per_sm;
     bool tc;
@@ -827,7 +838,15 @@ cudaError_t run_typed(const AttnArgs &a, const Plan &p, int max_rows, cudaStream
     if (e != cudaSuccess) return e;
     // One long sequence is cut into many pieces a unit, a batch into few. The
     // former's steps want every piece's read in flight at once if the SMs have
-    // one step each at most, and two CTAs an SM otherwise.
+    // one step each at most, and two CTAs an SM otherwise. Whole calls (us; few |
+    // <16, 6> | <32, 2>; dim 128, 8 key/value heads):
+    //   1 of 1,021, 4 rows       20.0 |  9.6 | 10.9   16 of 4,000, 4 rows   53.5 |  73.3 | 55.6
+    //   1 of 16,383, 4 rows      47.7 | 20.8 | 23.0   32 of 2,000, 4 rows   53.9 |  87.8 | 60.2
+    //   1 of 16,383, 32 rows     56.6 | 26.4 | 29.6   32 of 2,000, 32 rows  61.9 | 120.4 | 82.3
+    //   4 of 4,000, 16 rows      27.6 | 24.4 | 21.1   1 of 8,000, 128 rows  45.8 |  29.4 | 28.4
+    //   8 of 4,000, 4 rows       34.8 | 42.0 | 31.1   1 of 32,749, 256 rows 76.7 |  68.1 | 59.4
+    // (4 of 8,000 with 256 rows, 32 units: 61.7 | 91.8 | 68.0, where the rule's border
+    // lies too high.)
     const long long units = (long long)a.n * a.cache.n_kv_heads * ((max_rows + p.rows - 1) / p.rows);
     const long long steps = min((long long)a.grid - 1, units) * ((p.rows + 31) / 32);  // of 32 rows
     const int sms = a.grid / p.grid_per_sm;

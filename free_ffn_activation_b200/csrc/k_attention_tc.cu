@@ -25,9 +25,11 @@
 // MMAs 1,200 and its exponentials 1,024 of a scheduler's special-function unit; the
 // rest is the softmax warps' own chain (fetch 100, maximum 350 to 450, two waits of
 // 170), two warps a scheduler. Measured: 64 tokens of 32 heads over 32,749 tokens
-// 61.5 us (560 TFLOP/s; 6 us before the first scores, 7 us of joining), 16 sequences
-// with 40 to 64 tokens over 8,000 to 32,000 401 us (760 TFLOP/s; 473 us in long runs
-// at 1000 W, where the clock falls to 1.6 GHz).
+// 62 us (550 TFLOP/s; 6 us before the first scores, 7 us of joining, 28 tiles a CTA
+// 29 us; the other 20 are CTAs that end late: the mean SM is active for 72% of the
+// time), 16 sequences with 40 to 64 tokens over 8,000 to 32,000 420 us in short runs
+// (725 TFLOP/s), 470 to 500 us by GPU in long ones at 1000 W, where the clock falls
+// to 1.6 GHz.
 #include "attention.cuh"
 #include "umma.cuh"
 
@@ -192,7 +194,7 @@ __device__ __forceinline__ T uniform(T x) {
 // The queries into L2, a few lines a thread, by all CTAs together: where each
 // CTA's rows are is known only after the line, and its reads would then stand
 // behind the first stages of keys and values of all CTAs (64 drafted tokens of 32
-// heads over 32,749 tokens: 62.1 -> 61.5 us).
+// heads over 32,749 tokens: 62.1 -> 61.5 us when it was added).
 __device__ __forceinline__ void prefetch_queries(const AttnArgs &a, int D) {
     const unsigned per_row = a.n_heads * (D / 64);  // lines of 128 bytes
     const unsigned step = gridDim.x * blockDim.x;
@@ -458,8 +460,9 @@ __global__ void __launch_bounds__(Cfg<D, NWG>::THREADS, Cfg<D, NWG>::PER_SM)
         // A row of a stretch's tile: its drafted token and head, whether it exists. Worked
         // out anew where it is wanted (q, masks, outputs): kept over the loop of tiles, it
         // took registers that the scores then had to leave for local memory (16 sequences
-        // of 8,000 to 32,000 tokens: 427 -> 401 us). With one row group there is room for
-        // the token alone, which spares short units a division (ragged batch 41.9 -> 40.3).
+        // of 8,000 to 32,000 tokens in short runs: 427 -> 401 us at the time). With one row
+        // group there is room for the token alone, which spares short units a division
+        // (ragged batch 41.9 -> 40.3).
         struct Place {
             int tok, head;
             size_t row;

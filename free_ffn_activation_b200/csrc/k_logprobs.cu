@@ -14,8 +14,9 @@
 // no workspace and no second launch is needed, and the result does not depend
 // on timing.
 //
-// Measured on the device: 4,000 rows of 128,257 fp32 with the top 5 (2.05 GB) 319 us,
-// 6.4 TB/s, 98% of the rate of a copy; 64 rows of 151,936 bf16 with the top 20 17.3 us,
+// Measured on the device: 4,000 rows of 128,257 fp32 with the top 5 (2.05 GB) 319 us in
+// short runs, 6.4 TB/s, 98% of the rate of a copy, and 357 to 365 us in long ones (87%),
+// which power bounds; 64 rows of 151,936 bf16 with the top 20 17.3 us,
 // where the first loads, two selections and the cluster's join outweigh the 3 us of
 // reading; one row of 32,000 3.3 us. Sums of two elements an instruction were slower
 // (366 against 357 us for the first of these, with 512 threads).
@@ -328,6 +329,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logprobs(const Logp
     float flv = key_value(0);  // NaN: nothing is below it
     int steps = 0, refresh = 1;
     fetch(v0 + tid);
+// (two steps unrolled | one, us: 2,000 rows of 151,936 bf16 with the top 20 230 | 206,
+// of 32,000 with the top 5 65 | 54; without alternatives 107.8 | 110.6; 128,256 fp32
+// with the top 5 170 | 170, without 160.3 | 162.6)
 #pragma unroll(TOP && N == 8 ? 1 : 2)
     for (int vb = v0; vb < v1; vb += kStep) {
         const int v = vb + tid;
@@ -563,7 +567,7 @@ cudaError_t launch_dt(const LogprobArgs &a, bool narrow, int split, cudaStream_t
 //   64          17.4 |  20.1        8.8 |   8.3      15.2 |  16.2           9.7 |  7.8
 //   600         75.4 |  88.9       45.3 |  44.4      69.4 |  71.1          27.3 | 21.9
 //   2,000      206.5 | 203.2      121.1 | 107.7     185.1 | 171.0          71.6 | 52.4
-//   4,000                                           357   | 319
+//   4,000 (short runs)                              357   | 319
 bool narrow_rows(int rows, int vectors, int sms) { return rows >= 8 * sms || vectors <= 4096; }
 
 }  // namespace

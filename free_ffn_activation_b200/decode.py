@@ -166,7 +166,8 @@ class PagedCache:
 def cache_reserve(cache: PagedCache, seqs: torch.Tensor, n_new: torch.Tensor,
                   ok: torch.Tensor | None = None) -> None:
     """prox_cache_reserve: pages for n_new[i] tokens behind the committed ones
-    of sequence seqs[i] (int32 [n] each); ok uint8 [n] tells which got them."""
+    of sequence seqs[i] (int32 [n] each); ok uint8 [n] tells which got them (too few
+    free pages refuse an entry and those behind it, too many columns it alone)."""
     n, dev = seqs.numel(), cache.device
     a = (n, _ints(seqs, (n,), dev, "seqs"), _ints(n_new, (n,), dev, "n_new"),
          None if ok is None else _ints(ok, (n,), dev, "ok", torch.uint8))
@@ -205,7 +206,8 @@ def cache_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, *, share
 def cache_compact(cache: PagedCache, seqs: torch.Tensor, path: torch.Tensor, n_path: torch.Tensor,
                   ok: torch.Tensor | None = None) -> None:
     """prox_cache_compact: the drafted rows path[i][: n_path[i]] (ascending)
-    become committed tokens of seqs[i]; path int32 [n][max_path]."""
+    become committed tokens of seqs[i]; path int32 [n][max_path]; ok uint8 [n] tells
+    which paths were taken, each as a whole or not at all."""
     n, dev = seqs.numel(), cache.device
     if path.dim() != 2:
         raise ValueError("path must be [n][max_path]")
@@ -225,7 +227,7 @@ def cache_free(cache: PagedCache, seqs: torch.Tensor) -> None:
 
 
 def cache_status(cache: PagedCache) -> tuple[int, int]:
-    """(status, CACHE_* bits) of the cache's status word; clears it."""
+    """(status, CACHE_* bits) of the cache's status word; clears the bits returned."""
     flags = C.c_uint32()
     with _on(cache.device):
         st = _lib().prox_cache_status(cache._ref, _stream(cache.device), C.byref(flags))
@@ -254,7 +256,7 @@ def tree_attention(cache: PagedCache, layer: int, q: torch.Tensor, seqs: torch.T
     (rows cu_q[i] .. cu_q[i+1] - 1 belong to sequence seqs[i]) over one layer of
     the cache. tree int64 [rows][words] has the bits of the drafted tokens each
     row sees; None is a chain. scale defaults to head_dim ** -0.5. Rows behind
-    the last sequence are left as they are in out and lse."""
+    the last sequence are left as they are in out and lse. out may be q."""
     # (outputs made here are not checked, and made from sizes given one by one: the
     # shortest calls take less time on the GPU than on the host)
     dev, dim = cache.device, cache.head_dim

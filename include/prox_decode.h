@@ -169,9 +169,10 @@ prox_status prox_cache_status(const prox_cache *cache, void *stream, uint32_t *f
  * A row that sees no key (and every row of an entry that is left out) gets
  * out 0 and lse -inf; what a masked key or value
  * holds (NaN and infinities among it) has no influence. An infinite value that
- * is seen counts p_j v_j as any other: an infinity, or NaN where p_j is 0 (it
- * underflows in fp32 for a drafted token, in the cache's type for a committed
- * one; where it comes near that, parts of the keys may have seen it larger).
+ * is seen counts p_j v_j as any other: an infinity, or NaN where p_j is 0. That
+ * is where it underflows in fp32 for a drafted token, and in the cache's type
+ * for a committed one; close to it, which of the two comes out may depend on how
+ * the keys were divided among the blocks.
  * The drafted rows must be in the cache already (prox_cache_append). Rows
  * behind cu_q[n] are neither read nor written.
  *   q    : device, [rows][n_heads][head_dim] of the cache's type, rows
@@ -180,7 +181,7 @@ prox_status prox_cache_status(const prox_cache *cache, void *stream, uint32_t *f
  *          max_q rows (1 <= max_q <= 256).
  *   tree : device, uint64 [rows][tree_words] or NULL; tree_words >=
  *          ceil(max_q / 64). Bits d >= T are ignored.
- *   scale: > 0, and scale * log2(e) finite in fp32.
+ *   scale: > 0; scale * log2(e), and the scores times that, finite in fp32.
  *   out  : device, the cache's type, [rows][n_heads][head_dim], rows
  *          out_stride elements apart (as q_stride).
  *   lse  : device, fp32 [rows][n_heads], or NULL.
