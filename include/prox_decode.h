@@ -218,7 +218,8 @@ prox_status prox_tree_attention(const prox_cache *cache, int layer, int n, const
  *   logp   : device, fp32 [rows][n_tok];  entropy : device, fp32 [rows] or NULL.
  *   top_ids, top_logp : device, int32 / fp32 [rows][top_k],
  *            0 <= top_k <= min(64, vocab) (NULL if 0).
- * Sums in fp32 per thread and fp64 across threads, in a fixed order.
+ * Sums in fp32 per thread (of up to vocab / 256 terms, so off by 2^-24 for each
+ * at most) and in fp64 across threads, in a fixed order.
  */
 prox_status prox_logprobs(int rows, int vocab, int dtype, const void *logits, int64_t stride,
                           const int32_t *tokens, int n_tok, int top_k, float *logp, float *entropy,
