@@ -26,8 +26,8 @@
 // rest is the softmax warps' own chain (fetch 100, maximum 350 to 450, two waits of
 // 170), two warps a scheduler. Measured: 64 tokens of 32 heads over 32,749 tokens
 // 62 us (550 TFLOP/s; 6 us before the first scores, 7 us of joining, 28 tiles a CTA
-// 29 us; the other 20 are CTAs that end late: the mean SM is active for 71% of the
-// time), 16 sequences with 40 to 64 tokens over 8,000 to 32,000 420 us in short runs
+// 29 us; the other 20 are not accounted for by these: the mean SM is active for 71% of
+// the time, the slowest for 89%), 16 sequences with 40 to 64 tokens over 8,000 to 32,000 420 us in short runs
 // (725 TFLOP/s), 470 to 500 us by GPU in long ones at 1000 W, where the clock falls
 // to 1.6 GHz.
 #include "attention.cuh"
